@@ -74,6 +74,15 @@ _SIGNATURES = {
     "basiskv_decode_latents": (_I, [_DIMS, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I,
                                     _P, _P, _P, _SZ, _P]),
     "basiskv_outproj_sources": (_I, [_DIMS, _P, _I, _P, _P, _P, _SZ, _P]),
+    "basiskv_cache4_bytes": (_SZ, [_DIMS, _I]),
+    "basiskv_cache4_write": (_I, [_DIMS, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "basiskv_cache4_read": (_I, [_DIMS, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "basiskv_cache4_route": (_I, [_DIMS, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _SZ,
+                                  _P]),
+    "basiskv_cache4_attend": (_I, [_DIMS, _P, _P, _I, _P, _P, _P, _P, _I, _P, _P, _SZ, _P]),
+    "basiskv_window_workspace_size": (_SZ, [_DIMS, _I, _I, _I, _I]),
+    "basiskv_attend_window": (_I, [_DIMS, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _SZ,
+                                   _P]),
     "basiskv_read_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "basiskv_strerror": (ctypes.c_char_p, [_I]),
     "basiskv_launch_count": (ctypes.c_uint64, []),
@@ -224,6 +233,70 @@ def basiskv_outproj_sources(dims: Dims, a_src, n_src: int, W_fold, y, workspace,
     _check(load_library().basiskv_outproj_sources(
         ctypes.byref(dims), _ptr(a_src), n_src, _ptr(W_fold), _ptr(y), _ptr(workspace),
         _nbytes(workspace), _stream(stream)), "basiskv_outproj_sources")
+
+
+def cache4_bytes(dims: Dims, width: int) -> int:
+    """Bytes of one 4-bit cache of row width d, r_v or r_k (0: not supported)."""
+    return load_library().basiskv_cache4_bytes(ctypes.byref(dims), width)
+
+
+def basiskv_cache4_write(dims: Dims, k_new, z_new, e_new, n_new: int, seq_lens, lens_out,
+                         block_table, K4, Z4, E4, stream=None) -> None:
+    """Rounds rows of k, z and e (e_new and E4 may be None) to 4 bits into
+    their pages behind seq_lens; lens_out (seq_lens itself, another buffer or
+    None) receives the lengths after it."""
+    _check(load_library().basiskv_cache4_write(
+        ctypes.byref(dims), _ptr(k_new), _ptr(z_new), _ptr(e_new), n_new, _ptr(seq_lens),
+        _ptr(lens_out), _ptr(block_table), _ptr(K4), _ptr(Z4), _ptr(E4), _stream(stream)),
+        "basiskv_cache4_write")
+
+
+def basiskv_cache4_read(dims: Dims, first, count: int, seq_lens, block_table, K4, Z4, E4, k_out,
+                        z_out, e_out, stream=None) -> None:
+    """Reads tokens first[b] .. first[b] + count - 1 back as bf16 values (a
+    cache and its output may be None together)."""
+    _check(load_library().basiskv_cache4_read(
+        ctypes.byref(dims), _ptr(first), count, _ptr(seq_lens), _ptr(block_table), _ptr(K4),
+        _ptr(Z4), _ptr(E4), _ptr(k_out), _ptr(z_out), _ptr(e_out), _stream(stream)),
+        "basiskv_cache4_read")
+
+
+def basiskv_cache4_route(dims: Dims, q, seq_lens, max_seq_len: int, block_table, P_K, U_K, Z4,
+                         E4, top_k: int, page_scores, sel, workspace, stream=None) -> None:
+    """basiskv_route over 4-bit caches."""
+    _check(load_library().basiskv_cache4_route(
+        ctypes.byref(dims), _ptr(q), _ptr(seq_lens), max_seq_len, _ptr(block_table),
+        _ptr(P_K), _ptr(U_K), _ptr(Z4), _ptr(E4), top_k, _ptr(page_scores), _ptr(sel),
+        _ptr(workspace), _nbytes(workspace), _stream(stream)), "basiskv_cache4_route")
+
+
+def basiskv_cache4_attend(dims: Dims, q, seq_lens, max_seq_len: int, block_table, K4, Z4, sel,
+                          top_k: int, a_out, workspace, stream=None) -> None:
+    """basiskv_attend over 4-bit caches; a_out bf16 [B][Hq][r_v]."""
+    _check(load_library().basiskv_cache4_attend(
+        ctypes.byref(dims), _ptr(q), _ptr(seq_lens), max_seq_len, _ptr(block_table), _ptr(K4),
+        _ptr(Z4), _ptr(sel), top_k, _ptr(a_out), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)), "basiskv_cache4_attend")
+
+
+def window_workspace_size(dims: Dims, n_q: int, max_seq_len: int, sink_tokens: int,
+                          window: int) -> int:
+    """Bytes of workspace basiskv_attend_window needs (0: invalid arguments)."""
+    return load_library().basiskv_window_workspace_size(ctypes.byref(dims), n_q, max_seq_len,
+                                                        sink_tokens, window)
+
+
+def basiskv_attend_window(dims: Dims, q, n_q: int, seq_lens, max_seq_len: int, block_table,
+                          K_cache, Z_cache, sink_tokens: int, window: int, a_out, workspace,
+                          stream=None, cache4: bool = False) -> None:
+    """Attention of the last n_q tokens of every sequence over a sliding
+    window (0: everything) and the first sink_tokens tokens; bf16 or E4M3
+    caches by dims.cache_fp8, or 4-bit ones.  q bf16 [B][n_q][Hq][d], a_out
+    bf16 [B][n_q][Hq][r_v]."""
+    _check(load_library().basiskv_attend_window(
+        ctypes.byref(dims), _ptr(q), n_q, _ptr(seq_lens), max_seq_len, _ptr(block_table),
+        _ptr(K_cache), _ptr(Z_cache), int(cache4), sink_tokens, window, _ptr(a_out),
+        _ptr(workspace), _nbytes(workspace), _stream(stream)), "basiskv_attend_window")
 
 
 def read_device_status(stream=None) -> int:

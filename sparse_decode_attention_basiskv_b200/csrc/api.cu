@@ -198,6 +198,12 @@ int check_len_topk(const basiskv_dims* d, int top_k, int max_seq_len) {
 
 }  // namespace
 
+int basiskv::validate_dims(const basiskv_dims* d) { return check_dims(d); }
+int basiskv::validate_len_topk(const basiskv_dims* d, int top_k, int max_seq_len) {
+  return check_len_topk(d, top_k, max_seq_len);
+}
+bool basiskv::pdl_allowed() { return pdl_enabled(); }
+
 // Shape, length and top_k checks of the decode entry points (host only).
 int basiskv::validate_decode_shape(const basiskv_dims* d, int top_k, int max_seq_len) {
   const int rc = check_dims(d);
@@ -248,6 +254,15 @@ WsLayout ws_layout(const basiskv_dims* d, int top_k) {
   w.total = off;
   return w;
 }
+
+}  // namespace
+
+WsRegions basiskv::workspace_regions(const basiskv_dims* d, int top_k) {
+  const WsLayout w = ws_layout(d, top_k);
+  return {w.qt, w.scores, w.selp, w.partial, w.total};
+}
+
+namespace {
 
 int launch_status(cudaError_t e) {
   if (e == cudaSuccess) e = cudaGetLastError();

@@ -1,0 +1,320 @@
+// Entry points of basiskv_cache4.h and basiskv_window.h: argument checks
+// (host arithmetic, before any CUDA call) and launch sequences.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "../../include/basiskv_cache4.h"
+#include "../../include/basiskv_window.h"
+#include "cache4.cuh"
+#include "internal.h"
+#include "launch.cuh"
+
+using namespace basiskv;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+#define BKV_NEED(p, n)                                          \
+  do {                                                          \
+    if (!(p) || !aligned(p, n)) return BASISKV_ERR_INVALID_ARG; \
+  } while (0)
+#define BKV_MAY(p, n)                                          \
+  do {                                                         \
+    if ((p) && !aligned(p, n)) return BASISKV_ERR_INVALID_ARG; \
+  } while (0)
+
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? BASISKV_OK : BASISKV_ERR_LAUNCH_FAILED;
+}
+
+int check_cache4(const basiskv_dims* d) {
+  const int rc = validate_dims(d);
+  if (rc) return rc;
+  if (d->page_size != 16 && d->page_size != 32) return BASISKV_ERR_UNSUPPORTED_SHAPE;
+  if (d->cache_fp8) return BASISKV_ERR_INVALID_ARG;  // one element type
+  if ((d->route_page && d->route_page != d->page_size) ||
+      (d->route_r_v && d->route_r_v != d->r_v) || (d->route_r_k && d->route_r_k != d->r_k))
+    return BASISKV_ERR_UNSUPPORTED_SHAPE;
+  return BASISKV_OK;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws || !aligned(ws, 256)) return BASISKV_ERR_INVALID_ARG;
+  return have < need ? BASISKV_ERR_WORKSPACE_TOO_SMALL : BASISKV_OK;
+}
+
+// The arguments every attention over spans shares.
+SpanArgs span_args(const basiskv_dims* d, const basiskv_bf16* q, const int32_t* seq_lens,
+                   int max_seq_len, const int32_t* block_table, const void* K, const void* Z,
+                   basiskv_bf16* out, unsigned int* status) {
+  SpanArgs a{};
+  a.q = q;
+  a.K = static_cast<const uint8_t*>(K);
+  a.Z = static_cast<const uint8_t*>(Z);
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.out = out;
+  a.B = d->B;
+  a.Hq = d->Hq;
+  a.Hkv = d->Hkv;
+  a.G = d->Hq / d->Hkv;
+  a.d = d->d;
+  a.r_v = d->r_v;
+  a.S = d->page_size;
+  a.logS = d->page_size == 8 ? 3 : (d->page_size == 16 ? 4 : 5);
+  a.max_pages = d->max_pages_per_seq;
+  a.num_phys = d->num_phys_pages;
+  a.max_seq_len = max_seq_len;
+  a.zsplit = d->route_r_v ? d->route_r_v : d->r_v;
+  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)d->d));
+  a.status = status;
+  return a;
+}
+
+size_t span_partial_bytes(const basiskv_dims* d, int rows) {
+  return (span_slots(d->B, d->Hkv) * rows * (d->r_v + 2) * 4 + 255) & ~size_t(255);
+}
+
+int check_window(const basiskv_dims* d, int n_q, int max_seq_len, int sink, int window) {
+  if (!d || (d->cache_fp8 != 0 && d->cache_fp8 != 1)) return BASISKV_ERR_INVALID_ARG;
+  basiskv_dims plain = *d;  // the E4M3 router's and the routing page's limits do not apply
+  plain.cache_fp8 = 0;
+  plain.route_page = 0;
+  const int rc = validate_dims(&plain);
+  if (rc) return rc;
+  const long long cap = (long long)d->max_pages_per_seq * d->page_size;
+  if (max_seq_len < 1 || max_seq_len > cap || n_q < 1 || n_q > cap || sink < 0 || window < 0)
+    return BASISKV_ERR_INVALID_ARG;
+  return BASISKV_OK;
+}
+
+// Query tokens of one launch of the streaming kernel.
+int span_tokens(int n_q, int G) { return n_q * G <= kSpanMaxRows ? n_q : kSpanMaxRows / G; }
+
+size_t window_bytes(const basiskv_dims* d, int n_q) {
+  const int G = d->Hq / d->Hkv;
+  return span_partial_bytes(d, span_tokens(n_q, G) * G);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t basiskv_cache4_bytes(const basiskv_dims* dims, int width) {
+  if (check_cache4(dims) != BASISKV_OK) return 0;
+  if (width != dims->d && width != dims->r_v && width != dims->r_k) return 0;
+  return (size_t)dims->num_phys_pages * dims->Hkv * q4_tile_bytes(dims->page_size, width);
+}
+
+int basiskv_cache4_write(const basiskv_dims* dims, const basiskv_bf16* k_new,
+                         const basiskv_bf16* z_new, const basiskv_bf16* e_new, int n_new,
+                         const int32_t* seq_lens, int32_t* lens_out, const int32_t* block_table,
+                         uint8_t* K4, uint8_t* Z4, uint8_t* E4, void* stream) {
+  int rc = check_cache4(dims);
+  if (rc) return rc;
+  if (n_new < 1 || (long long)n_new > (long long)dims->max_pages_per_seq * dims->page_size)
+    return BASISKV_ERR_INVALID_ARG;
+  BKV_NEED(k_new, 16);
+  BKV_NEED(z_new, 16);
+  BKV_NEED(K4, 16);
+  BKV_NEED(Z4, 16);
+  if (!e_new != !E4) return BASISKV_ERR_INVALID_ARG;
+  BKV_MAY(e_new, 16);
+  BKV_MAY(E4, 16);
+  BKV_NEED(seq_lens, 4);
+  BKV_MAY(lens_out, 4);
+  BKV_NEED(block_table, 4);
+  Cache4Args a{};
+  a.status = device_status_ptr();
+  if (!a.status) return BASISKV_ERR_CUDA;
+  a.rows[0] = k_new, a.rows[1] = z_new, a.rows[2] = e_new;
+  a.cache[0] = K4, a.cache[1] = Z4, a.cache[2] = E4;
+  a.width[0] = dims->d, a.width[1] = dims->r_v, a.width[2] = dims->r_k;
+  for (int i = 0; i < 3; ++i) a.chunks[i] = a.rows[i] ? dims->Hkv * a.width[i] / 8 : 0;
+  a.seq_lens = seq_lens;
+  const bool in_place = lens_out == seq_lens;
+  a.lens_out = in_place ? nullptr : lens_out;
+  a.block_table = block_table;
+  a.B = dims->B, a.n = n_new, a.Hkv = dims->Hkv, a.S = dims->page_size;
+  a.max_pages = dims->max_pages_per_seq, a.num_phys = dims->num_phys_pages;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = status_of(launch_cache4_write(a, st, pdl_allowed()));
+  if (rc || !in_place) return rc;
+  // in place, the lengths move only once every CTA has read them
+  AppendArgs b{};
+  b.seq_lens = seq_lens;
+  b.seq_lens_out = lens_out;
+  b.B = dims->B, b.n_new = n_new, b.max_pages = dims->max_pages_per_seq, b.S = dims->page_size;
+  b.status = a.status;
+  return status_of(launch_bump_lengths(b, st, pdl_allowed()));
+}
+
+int basiskv_cache4_read(const basiskv_dims* dims, const int32_t* first, int count,
+                        const int32_t* seq_lens, const int32_t* block_table, const uint8_t* K4,
+                        const uint8_t* Z4, const uint8_t* E4, basiskv_bf16* k_out,
+                        basiskv_bf16* z_out, basiskv_bf16* e_out, void* stream) {
+  int rc = check_cache4(dims);
+  if (rc) return rc;
+  if (count < 1 || (long long)count > (long long)dims->max_pages_per_seq * dims->page_size)
+    return BASISKV_ERR_INVALID_ARG;
+  BKV_NEED(first, 4);
+  BKV_NEED(seq_lens, 4);
+  BKV_NEED(block_table, 4);
+  if (!k_out != !K4 || !z_out != !Z4 || !e_out != !E4 || (!k_out && !z_out && !e_out))
+    return BASISKV_ERR_INVALID_ARG;
+  BKV_MAY(K4, 16);
+  BKV_MAY(Z4, 16);
+  BKV_MAY(E4, 16);
+  BKV_MAY(k_out, 16);
+  BKV_MAY(z_out, 16);
+  BKV_MAY(e_out, 16);
+  Cache4Args a{};
+  a.status = device_status_ptr();
+  if (!a.status) return BASISKV_ERR_CUDA;
+  a.out[0] = k_out, a.out[1] = z_out, a.out[2] = e_out;
+  a.cache[0] = const_cast<uint8_t*>(K4);
+  a.cache[1] = const_cast<uint8_t*>(Z4);
+  a.cache[2] = const_cast<uint8_t*>(E4);
+  a.width[0] = dims->d, a.width[1] = dims->r_v, a.width[2] = dims->r_k;
+  for (int i = 0; i < 3; ++i) a.chunks[i] = a.out[i] ? dims->Hkv * a.width[i] / 8 : 0;
+  a.first = first;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.B = dims->B, a.n = count, a.Hkv = dims->Hkv, a.S = dims->page_size;
+  a.max_pages = dims->max_pages_per_seq, a.num_phys = dims->num_phys_pages;
+  return status_of(launch_cache4_read(a, static_cast<cudaStream_t>(stream), pdl_allowed()));
+}
+
+int basiskv_cache4_route(const basiskv_dims* dims, const basiskv_bf16* q, const int32_t* seq_lens,
+                         int max_seq_len, const int32_t* block_table, const basiskv_bf16* P_K,
+                         const basiskv_bf16* U_K, const uint8_t* Z4, const uint8_t* E4, int top_k,
+                         float* page_scores, int32_t* sel, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  int rc = check_cache4(dims);
+  if (rc) return rc;
+  rc = validate_len_topk(dims, top_k, max_seq_len);
+  if (rc) return rc;
+  BKV_NEED(q, 16);
+  BKV_NEED(seq_lens, 4);
+  BKV_NEED(block_table, 4);
+  BKV_NEED(P_K, 16);
+  BKV_NEED(U_K, 16);
+  BKV_NEED(Z4, 16);
+  BKV_NEED(E4, 16);
+  if (!sel && !page_scores) return BASISKV_ERR_INVALID_ARG;  // nothing to write
+  BKV_MAY(sel, 4);
+  BKV_MAY(page_scores, 4);
+  const WsRegions L = workspace_regions(dims, top_k);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool pdl = pdl_allowed();
+  unsigned int* status = device_status_ptr();
+  if (!status) return BASISKV_ERR_CUDA;
+  float* qt = reinterpret_cast<float*>(ws + L.qt);
+  FoldQArgs f{q, P_K, U_K, qt, dims->B, dims->Hq, dims->Hkv, dims->d, dims->r_v, dims->r_k};
+  rc = status_of(launch_fold_query(f, st, pdl));
+  if (rc) return rc;
+  Route4Args r{};
+  r.qt = qt;
+  r.Z = Z4;
+  r.E = E4;
+  r.seq_lens = seq_lens;
+  r.block_table = block_table;
+  r.scores = page_scores ? page_scores : reinterpret_cast<float*>(ws + L.scores);
+  r.B = dims->B, r.Hq = dims->Hq, r.Hkv = dims->Hkv, r.G = dims->Hq / dims->Hkv;
+  r.r_v = dims->r_v, r.r_k = dims->r_k, r.S = dims->page_size;
+  r.max_pages = dims->max_pages_per_seq, r.num_phys = dims->num_phys_pages;
+  r.max_seq_len = max_seq_len;
+  r.status = status;
+  rc = status_of(launch_route4(r, st, pdl));
+  if (rc || !sel) return rc;
+  const int n_sink = dims->sink_pages == 0 ? 1 : (dims->sink_pages < 0 ? 0 : dims->sink_pages);
+  SelectArgs s{r.scores, seq_lens, sel, dims->B, dims->Hkv, dims->page_size,
+               dims->max_pages_per_seq, top_k, max_seq_len, 0, block_table,
+               reinterpret_cast<int32_t*>(ws + L.selp), n_sink,
+               dims->recent_pages == 0 ? 1 : dims->recent_pages, 1};
+  return status_of(launch_select(s, st, pdl));
+}
+
+int basiskv_cache4_attend(const basiskv_dims* dims, const basiskv_bf16* q,
+                          const int32_t* seq_lens, int max_seq_len, const int32_t* block_table,
+                          const uint8_t* K4, const uint8_t* Z4, const int32_t* sel, int top_k,
+                          basiskv_bf16* a_out, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int rc = check_cache4(dims);
+  if (rc) return rc;
+  rc = validate_len_topk(dims, top_k, max_seq_len);
+  if (rc) return rc;
+  BKV_NEED(q, 16);
+  BKV_NEED(seq_lens, 4);
+  BKV_NEED(block_table, 4);
+  BKV_NEED(K4, 16);
+  BKV_NEED(Z4, 16);
+  BKV_NEED(sel, 4);
+  BKV_NEED(a_out, 16);
+  const WsRegions L = workspace_regions(dims, top_k);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc) return rc;
+  unsigned int* status = device_status_ptr();
+  if (!status) return BASISKV_ERR_CUDA;
+  SpanArgs a = span_args(dims, q, seq_lens, max_seq_len, block_table, K4, Z4, a_out, status);
+  a.sel = sel;
+  a.top_k = top_k;
+  a.n_tot = a.n_q = 1;
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.partial);
+  return status_of(launch_span_q4(a, static_cast<cudaStream_t>(stream), pdl_allowed()));
+}
+
+size_t basiskv_window_workspace_size(const basiskv_dims* dims, int n_q, int max_seq_len,
+                                     int sink_tokens, int window) {
+  if (check_window(dims, n_q, max_seq_len, sink_tokens, window) != BASISKV_OK) return 0;
+  return window_bytes(dims, n_q);
+}
+
+int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n_q,
+                          const int32_t* seq_lens, int max_seq_len, const int32_t* block_table,
+                          const void* K_cache, const void* Z_cache, int cache4, int sink_tokens,
+                          int window, basiskv_bf16* a_out, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  int rc = check_window(dims, n_q, max_seq_len, sink_tokens, window);
+  if (rc) return rc;
+  if (cache4 != 0 && cache4 != 1) return BASISKV_ERR_INVALID_ARG;
+  if (cache4) {
+    rc = check_cache4(dims);
+    if (rc) return rc;
+  }
+  BKV_NEED(q, 16);
+  BKV_NEED(seq_lens, 4);
+  BKV_NEED(block_table, 4);
+  BKV_NEED(K_cache, 16);
+  BKV_NEED(Z_cache, 16);
+  BKV_NEED(a_out, 16);
+  rc = check_workspace(workspace, workspace_bytes, window_bytes(dims, n_q));
+  if (rc) return rc;
+  unsigned int* status = device_status_ptr();
+  if (!status) return BASISKV_ERR_CUDA;
+  SpanArgs a = span_args(dims, q, seq_lens, max_seq_len, block_table, K_cache, Z_cache, a_out,
+                         status);
+  a.sink = sink_tokens < max_seq_len ? sink_tokens : max_seq_len;
+  a.window = window < max_seq_len ? window : 0;  // it holds every token
+  a.partial = static_cast<float*>(workspace);
+  a.n_tot = n_q;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool pdl = pdl_allowed();
+  const int step = span_tokens(n_q, a.G);
+  for (int j = 0; j < n_q; j += step) {
+    a.j0 = j;
+    a.n_q = n_q - j < step ? n_q - j : step;
+    rc = status_of(cache4 ? launch_span_q4(a, st, pdl)
+                          : dims->cache_fp8 ? launch_span_e4m3(a, st, pdl)
+                                            : launch_span_bf16(a, st, pdl));
+    if (rc) return rc;
+  }
+  return BASISKV_OK;
+}
+
+}  // extern "C"

@@ -167,6 +167,27 @@ __device__ __forceinline__ float4 lds128f(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("{ .reg .u8 t; ld.shared.u8 t, [%1]; cvt.u32.u8 %0, t; }" : "=r"(v) : "r"(addr));
+  return v;
+}
+
 // The TMA swizzle modes XOR address bits [4, 4+b) with bits [7, 7+b):
 // b = 1 (32B), 2 (64B), 3 (128B).  `mask` = (1 << b) - 1.  Valid for boxes
 // whose shared-memory base is aligned to the swizzle repeat (256/512/1024 B).
@@ -381,6 +402,21 @@ __device__ __forceinline__ void cp_async4(void* smem_dst, const void* gmem_src) 
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 16-byte asynchronous copy to a shared address; with ok false the
+// destination is zeroed and the source (any valid address) is not read.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool ok = true) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+
+// 2^x (ex2.approx: 2 ulp; denormal results are zero).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ------------------------------------------------------------- PDL control

@@ -235,4 +235,72 @@ struct FoldOutArgs {
 };
 cudaError_t launch_fold_outproj(const FoldOutArgs& a, cudaStream_t st);
 
+// ------------------------------------------------------------ 4-bit caches
+struct Cache4Args {
+  const uint16_t* rows[3];  // write: k, z, e rows [B][n][Hkv][w] bf16
+  uint16_t* out[3];         // read: the same layout
+  uint8_t* cache[3];        // 4-bit tiles (cache4.cuh)
+  int width[3], chunks[3];  // w, and Hkv * w / 8 (0: the part is absent)
+  const int32_t* seq_lens;
+  const int32_t* first;  // read: first token of each sequence
+  int32_t* lens_out;     // write: lengths after it (null: not written here)
+  const int32_t* block_table;
+  int B, n, Hkv, S, max_pages, num_phys;
+  unsigned int* status;
+};
+cudaError_t launch_cache4_write(const Cache4Args& a, cudaStream_t st, bool pdl);
+cudaError_t launch_cache4_read(const Cache4Args& a, cudaStream_t st, bool pdl);
+
+struct Route4Args {
+  const float* qt;   // folded queries [B][Hq][r_v + r_k]
+  const uint8_t* Z;  // 4-bit tiles
+  const uint8_t* E;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  float* scores;  // [B][Hkv][max_pages]
+  int B, Hq, Hkv, G, r_v, r_k, S, max_pages, num_phys, max_seq_len;
+  unsigned int* status;
+};
+cudaError_t launch_route4(const Route4Args& a, cudaStream_t st, bool pdl);
+
+// ----------------------------------------------- attention over token spans
+// Attention of the query rows j0 .. j0 + n_q - 1 (of n_tot per sequence, the
+// last of them at position seq_lens[b] - 1) over a sliding window with
+// sinks, or (sel set, n_tot = 1) over selected pages.
+enum SpanFormat { kSpanBf16 = 0, kSpanE4m3 = 1, kSpanQ4 = 2 };
+struct SpanArgs {
+  const uint16_t* q;  // [B][n_tot][Hq][d]
+  const uint8_t* K;
+  const uint8_t* Z;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  const int32_t* sel;  // [B][Hkv][top_k] or null
+  float* partial;      // span_slots() * rows * (r_v + 2) floats
+  uint16_t* out;       // [B][n_tot][Hq][r_v] bf16
+  int B, Hq, Hkv, G, d, r_v, S, logS, max_pages, num_phys, max_seq_len, top_k;
+  int n_tot, j0, n_q;
+  int sink, window;  // window 0: everything
+  int zsplit;
+  float scale_log2;
+  unsigned int* status;
+};
+constexpr int kSpanMaxCtas = 1024;
+constexpr int kSpanMaxRows = 16;
+// CTAs of the launch for these arguments (a rule on the shape and the bound
+// max_seq_len only) and the partial slots it may write.
+inline size_t span_slots(int B, int Hkv) { return (size_t)kSpanMaxCtas + (size_t)B * Hkv; }
+cudaError_t launch_span_bf16(const SpanArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_span_e4m3(const SpanArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_span_q4(const SpanArgs& a, cudaStream_t st, bool pdl);
+
+// Used by the entry points outside api.cu.
+int validate_dims(const basiskv_dims* d);
+int validate_len_topk(const basiskv_dims* d, int top_k, int max_seq_len);
+bool pdl_allowed();
+// Regions of the shared workspace layout (byte offsets).
+struct WsRegions {
+  size_t qt, scores, selp, partial, total;
+};
+WsRegions workspace_regions(const basiskv_dims* d, int top_k);
+
 }  // namespace basiskv
