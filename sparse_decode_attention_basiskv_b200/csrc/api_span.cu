@@ -90,12 +90,28 @@ int check_window(const basiskv_dims* d, int n_q, int max_seq_len, int sink, int 
   return BASISKV_OK;
 }
 
-// Query tokens of one launch of the streaming kernel.
-int span_tokens(int n_q, int G) { return n_q * G <= kSpanMaxRows ? n_q : kSpanMaxRows / G; }
+// Up to kSpanMaxRows query rows a group are streamed, more go to the tensor
+// cores.
+bool window_streams(const basiskv_dims* d, int n_q) {
+  return n_q <= kSpanMaxRows / (d->Hq / d->Hkv);
+}
 
-size_t window_bytes(const basiskv_dims* d, int n_q) {
+// The mask with bounds that cover the whole context written as such.
+struct Mask {
+  int sink, window;
+};
+Mask window_mask(int max_seq_len, int sink, int window) {
+  return {sink < max_seq_len ? sink : max_seq_len, window < max_seq_len ? window : 0};
+}
+
+size_t window_bytes(const basiskv_dims* d, int n_q, int max_seq_len, int sink, int window) {
   const int G = d->Hq / d->Hkv;
-  return span_partial_bytes(d, span_tokens(n_q, G) * G);
+  if (window_streams(d, n_q)) return span_partial_bytes(d, n_q * G);
+  const Mask m = window_mask(max_seq_len, sink, window);
+  const int items = span_tc_items(d->B, d->Hkv, G, n_q);
+  const int nsplit = span_tc_splits(items, n_q, max_seq_len, m.sink, m.window);
+  const size_t n = span_tc_partial_bytes(items, nsplit, d->r_v);
+  return n > 256 ? (n + 255) & ~size_t(255) : 256;
 }
 
 }  // namespace
@@ -272,7 +288,7 @@ int basiskv_cache4_attend(const basiskv_dims* dims, const basiskv_bf16* q,
 size_t basiskv_window_workspace_size(const basiskv_dims* dims, int n_q, int max_seq_len,
                                      int sink_tokens, int window) {
   if (check_window(dims, n_q, max_seq_len, sink_tokens, window) != BASISKV_OK) return 0;
-  return window_bytes(dims, n_q);
+  return window_bytes(dims, n_q, max_seq_len, sink_tokens, window);
 }
 
 int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n_q,
@@ -293,28 +309,27 @@ int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n
   BKV_NEED(K_cache, 16);
   BKV_NEED(Z_cache, 16);
   BKV_NEED(a_out, 16);
-  rc = check_workspace(workspace, workspace_bytes, window_bytes(dims, n_q));
+  rc = check_workspace(workspace, workspace_bytes,
+                       window_bytes(dims, n_q, max_seq_len, sink_tokens, window));
   if (rc) return rc;
   unsigned int* status = device_status_ptr();
   if (!status) return BASISKV_ERR_CUDA;
   SpanArgs a = span_args(dims, q, seq_lens, max_seq_len, block_table, K_cache, Z_cache, a_out,
                          status);
-  a.sink = sink_tokens < max_seq_len ? sink_tokens : max_seq_len;
-  a.window = window < max_seq_len ? window : 0;  // it holds every token
+  const Mask m = window_mask(max_seq_len, sink_tokens, window);
+  a.sink = m.sink;
+  a.window = m.window;
   a.partial = static_cast<float*>(workspace);
-  a.n_tot = n_q;
+  a.n_tot = a.n_q = n_q;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool pdl = pdl_allowed();
-  const int step = span_tokens(n_q, a.G);
-  for (int j = 0; j < n_q; j += step) {
-    a.j0 = j;
-    a.n_q = n_q - j < step ? n_q - j : step;
-    rc = status_of(cache4 ? launch_span_q4(a, st, pdl)
-                          : dims->cache_fp8 ? launch_span_e4m3(a, st, pdl)
-                                            : launch_span_bf16(a, st, pdl));
-    if (rc) return rc;
-  }
-  return BASISKV_OK;
+  if (window_streams(dims, n_q))
+    return status_of(cache4 ? launch_span_q4(a, st, pdl)
+                            : dims->cache_fp8 ? launch_span_e4m3(a, st, pdl)
+                                              : launch_span_bf16(a, st, pdl));
+  return status_of(cache4 ? launch_span_tc_q4(a, st, pdl)
+                          : dims->cache_fp8 ? launch_span_tc_e4m3(a, st, pdl)
+                                            : launch_span_tc_bf16(a, st, pdl));
 }
 
 }  // extern "C"

@@ -293,6 +293,28 @@ cudaError_t launch_span_bf16(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_e4m3(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_q4(const SpanArgs& a, cudaStream_t st, bool pdl);
 
+// Prompt form (tensor cores; j0 = 0, n_q = n_tot, no selection): work items
+// of two row tiles, each cut into nsplit runs of KV tiles while the items
+// alone would leave SMs idle.
+inline int span_tc_items(int B, int Hkv, int G, int n_tot) {
+  const int tq2 = 256 / G;
+  return B * Hkv * ((n_tot + tq2 - 1) / tq2);
+}
+inline int span_tc_splits(int items, int n_tot, int max_seq_len, int sink, int window) {
+  long long span = max_seq_len;
+  if (window > 0 && (long long)window + n_tot + sink < span) span = window + n_tot + sink;
+  long long most = span / 512 > 0 ? span / 512 : 1;  // at least 4 KV tiles a run
+  long long n = 2 * (long long)num_sms() / items;
+  if (n > most) n = most;
+  return n > 1 ? (int)n : 1;
+}
+inline size_t span_tc_partial_bytes(int items, int nsplit, int r_v) {
+  return nsplit > 1 ? (size_t)items * nsplit * 256 * (r_v + 2) * 4 : 0;
+}
+cudaError_t launch_span_tc_bf16(const SpanArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_span_tc_e4m3(const SpanArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_span_tc_q4(const SpanArgs& a, cudaStream_t st, bool pdl);
+
 // Used by the entry points outside api.cu.
 int validate_dims(const basiskv_dims* d);
 int validate_len_topk(const basiskv_dims* d, int top_k, int max_seq_len);

@@ -1,0 +1,637 @@
+// Attention of many query rows over a sliding window with sinks on the
+// 5th-generation tensor cores: prompt chunks, and drafts of more rows than
+// the streaming kernel takes (instances: span_tc_bf16.cu, span_tc_e4m3.cu,
+// span_tc_q4.cu).
+//
+//   a[row] = sum_t p_t z_t,  p = softmax over the row's tokens of
+//   (q . K_t) / sqrt(d)
+//
+// A work item is (sequence, KV head, two tiles of 128 rows).  A row is a query
+// token and a head of the group (token-major), so the group's heads share each
+// Key and latent that is loaded, and a tile spans only 128 / G tokens of the
+// band.  Per 128-token KV tile and row tile: S = Q K^T (tcgen05, both operands
+// in shared memory), P = exp2(S - m) (registers), O += P Z (A from tensor
+// memory).  2 * 128 * 128 * (d + r_v) multiply-adds and 2 * 128 * 128
+// exponentials a KV tile: at d 128, r_v 64 the tensor cores need about 1540
+// clocks and the 16 exponentials a clock 2048, so the exponentials bound it.
+//
+// Roles (16 warps, one CTA an SM): warps 0-3 and 4-7 hold the softmax of one
+// row tile each, a thread a row (no shuffles), and rescale O, seldom: the
+// reference maximum moves only when the row's maximum has passed it by 8 in
+// log2; warps 8-11 bring in the KV tiles page by page into the swizzled layout
+// (bf16 by cp.async; E4M3 and 4-bit rows widened to f16 on the way, exactly);
+// one thread of warp 12 issues the MMAs, row tile 1's while row tile 0's
+// softmax runs and the other way round.  Tensor memory: S 2 x 128 columns (P
+// over the first 64 of each), O 2 x 128.
+//
+// Few items: the KV tiles of an item are cut into nsplit runs, whose partial
+// sums span_tc_merge_kernel joins.
+#pragma once
+
+#include "cache4.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "tcgen05.cuh"
+
+namespace basiskv {
+namespace {
+
+constexpr int kTcThreads = 512;
+constexpr int kTcRows = 256;  // two row tiles
+constexpr float kTcSlack = 8.f;
+
+template <int D, int RV>
+struct TcGeom {
+  static constexpr int kQBytes = kTcRows * D * 2;
+  static constexpr int kKBytes = 128 * D * 2;
+  static constexpr int kZBlocks = (RV + 63) / 64;  // 64-column blocks
+  static constexpr int kZBytes = kZBlocks * 128 * 128;
+  static constexpr int kStages = RV <= 64 ? 3 : 2;
+  static constexpr size_t kSmem = 1024 + kQBytes + kStages * (size_t)(kKBytes + kZBytes);
+};
+
+// One item's place and its KV tiles (128 tokens each): the sinks', then the
+// window's.
+struct TcItem {
+  int b, g, j0;         // first query token of the item
+  int pos0;             // its position
+  int live_end;         // no row sees a token from here on
+  int lo_first;         // first window token of the first row
+  int n_sink, tile0, n; // KV tiles
+};
+__device__ __forceinline__ TcItem tc_item(const SpanArgs& a, int item) {
+  TcItem x;
+  const int tq2 = kTcRows / a.G, njt = (a.n_tot + tq2 - 1) / tq2;
+  const int bg = item % (a.B * a.Hkv);
+  // the last tiles of a chunk see the most tokens: they go first
+  x.j0 = (njt - 1 - item / (a.B * a.Hkv)) * tq2;
+  x.b = bg / a.Hkv;
+  x.g = bg - x.b * a.Hkv;
+  int T = a.seq_lens[x.b];
+  if (T < 0 || T > a.max_seq_len) {
+    if (threadIdx.x == 0) raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
+    T = 0;
+  }
+  x.pos0 = T - a.n_tot + x.j0;
+  const int last = min(x.pos0 + tq2, T) - 1;
+  x.live_end = T > 0 ? last + 1 : 0;
+  x.lo_first = a.window > 0 ? max(0, max(x.pos0, 0) - a.window + 1) : 0;
+  if (x.live_end <= 0) {
+    x.n_sink = x.tile0 = x.n = 0;
+  } else {
+    x.tile0 = x.lo_first >> 7;
+    x.n_sink = min((a.sink + 127) >> 7, x.tile0);
+    x.n = x.n_sink + (last >> 7) - x.tile0 + 1;
+  }
+  return x;
+}
+__device__ __forceinline__ int tc_tile(const TcItem& x, int i) {
+  return i < x.n_sink ? i : x.tile0 + i - x.n_sink;
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of 128-byte swizzled rows
+// (64 16-bit columns each; the 64-column blocks lie 16 KB apart).
+__device__ __forceinline__ uint32_t tc_off(int r, int c) {
+  return (uint32_t)((c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z,
+                                       uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+
+template <int FMT, int D, int RV>
+__global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int nsplit) {
+  using Gm = TcGeom<D, RV>;
+  constexpr int NST = Gm::kStages;
+  constexpr bool BF = FMT == kSpanBf16;
+  extern __shared__ uint8_t tc_smem_raw[];
+  uint8_t* smem = align_smem_1k(tc_smem_raw);
+  __shared__ uint64_t bars[4 * NST + 6];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float row_scale[kTcRows];
+  uint64_t *kfull = bars, *kempty = bars + NST, *zfull = bars + 2 * NST, *zempty = bars + 3 * NST;
+  uint64_t *sfull = bars + 4 * NST, *pfull = sfull + 2, *ofull = sfull + 4;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sq = smem_u32(smem), sk = sq + Gm::kQBytes, sz = sk + NST * Gm::kKBytes;
+
+  if (tid == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&kfull[s], 128);
+      mbar_init(&zfull[s], 128);
+      mbar_init(&kempty[s], 1);
+      mbar_init(&zempty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pfull[t], 128);
+      mbar_init(&ofull[t], 1);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const TcItem it = tc_item(a, blockIdx.x / nsplit);
+  const int split = blockIdx.x % nsplit;
+  const int i0 = (int)((long long)it.n * split / nsplit);
+  const int n = (int)((long long)it.n * (split + 1) / nsplit) - i0;
+  const int tq = 128 / a.G;
+  const int rows = min(kTcRows, (a.n_tot - it.j0) * a.G);  // live rows of the item
+  const int nt = rows > 128 ? 2 : 1;                       // row tiles
+
+  // ---- queries into the swizzled layout, D / 8 lanes a row
+  {
+    constexpr int QC = D / 8;
+    for (int i = tid; i < kTcRows * QC; i += kTcThreads) {
+      const int r = i / QC, c = i - r * QC;
+      const int j = r / a.G, h = r - j * a.G;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows)
+        v = __ldg(reinterpret_cast<const uint4*>(
+            a.q + (((size_t)it.b * a.n_tot + it.j0 + j) * a.Hq + it.g * a.G + h) * D + 8 * c));
+      float scale = 1.f;
+      if constexpr (!BF) {
+        // f16 of the row times a power of two (largest magnitude in [2^14, 2^15))
+        uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = bf16x2_to_f2(u[k]);
+          m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+#pragma unroll
+        for (int o = 1; o < QC; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int ex = m > 0.f ? (int)((__float_as_uint(m) >> 23) & 0xffu) - 126 : 15;
+        const int sh = max(-126, min(126, 15 - ex));
+        const float sc = __uint_as_float((uint32_t)(127 + sh) << 23);
+        scale = __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = bf16x2_to_f2(u[k]);
+          const __half2 hh = __floats2half2_rn(f.x * sc, f.y * sc);
+          u[k] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        v = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+      const int t = r >> 7;
+      sts128(sq + t * (Gm::kQBytes / 2) + tc_off(r & 127, c), v.x, v.y, v.z, v.w);
+      if (c == 0) row_scale[r] = scale;
+    }
+  }
+  fence_proxy_async();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abrt = &abort_flag;
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------ MMA issue
+    if (tid == 12 * 32 && n > 0) {
+      constexpr uint32_t id_qk = tc_idesc(128, 128, BF, false);
+      constexpr uint32_t id_pv = tc_idesc(128, RV, BF, true);
+      auto qk = [&](int t, int i) {
+        const uint32_t qb = sq + t * (Gm::kQBytes / 2), kb = sk + (i % NST) * Gm::kKBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_ss(tmem + 128 * t, tc_sdesc(qb + (k >> 2) * 16384 + (k & 3) * 32),
+                    tc_sdesc(kb + (k >> 2) * 16384 + (k & 3) * 32), id_qk, k > 0);
+        tc_commit_to(&sfull[t]);
+      };
+      auto pv = [&](int t, int i) {
+        const uint32_t zb = sz + (i % NST) * Gm::kZBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, tc_sdesc(zb + k * 2048, 16384),
+                    id_pv, i > 0 || k > 0);
+        tc_commit_to(&ofull[t]);
+      };
+      bool ok = mbar_wait_or_abort(&kfull[0], 0, a.status, abrt);
+      if (ok) {
+        tc_fence_after_sync();
+        for (int t = 0; t < nt; ++t) qk(t, 0);
+        tc_commit_to(&kempty[0]);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        for (int t = 0; ok && t < nt; ++t) {
+          ok = mbar_wait_or_abort(&pfull[t], i & 1, a.status, abrt);
+          if (ok && t == 0)
+            ok = mbar_wait_or_abort(&zfull[i % NST], (i / NST) & 1, a.status, abrt);
+          if (!ok) break;
+          tc_fence_after_sync();
+          pv(t, i);
+          if (t == nt - 1) tc_commit_to(&zempty[i % NST]);
+          if (i + 1 < n) {
+            if (t == 0) {
+              ok = mbar_wait_or_abort(&kfull[(i + 1) % NST], ((i + 1) / NST) & 1, a.status, abrt);
+              if (!ok) break;
+              tc_fence_after_sync();
+            }
+            qk(t, i + 1);
+            if (t == nt - 1) tc_commit_to(&kempty[(i + 1) % NST]);
+          }
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- loaders
+    const int lt = tid - 256;  // 0 .. 127
+    // tokens some row of the item sees; the rest of a tile is zeroed
+    auto seen = [&](int t) { return t < it.live_end && (t >= it.lo_first || t < a.sink); };
+    // The tile row of token t, -1 when there is nothing to read.
+    auto tile_row = [&](int t) -> int {
+      if (!seen(t)) return -1;
+      const int p = t >> a.logS;
+      const int pp = p < a.max_pages ? __ldg(a.block_table + (size_t)it.b * a.max_pages + p) : -1;
+      if (pp < 0 || pp >= a.num_phys) {
+        raise_status(a.status, BASISKV_DEV_BAD_PAGE);
+        return -1;
+      }
+      return ((pp * a.Hkv + it.g) << a.logS) + (t & (a.S - 1));
+    };
+    if constexpr (BF) {
+      // Rows 32 w .. 32 w + 31 of a tile are warp w's: lane l looks row l's
+      // place up, and the lanes then copy whole rows together.
+      const int w = lt >> 5;
+      constexpr int KC = D / 8, ZC = RV / 8;
+      auto copy_k = [&](int i, int row) {
+        const uint32_t dst = sk + (i % NST) * Gm::kKBytes;
+#pragma unroll
+        for (int x = 0; x < KC; ++x) {
+          const int y = 32 * x + lane, r = y / KC, c = y % KC;
+          const int tr = __shfl_sync(0xffffffffu, row, r);
+          cp_async16_or_zero(dst + tc_off(32 * w + r, c),
+                             a.K + (tr < 0 ? 0 : ((size_t)tr * D + 8 * c) * 2), tr >= 0);
+        }
+      };
+      auto copy_z = [&](int i, int row) {
+        const uint32_t dst = sz + (i % NST) * Gm::kZBytes;
+#pragma unroll
+        for (int x = 0; x < ZC; ++x) {
+          const int y = 32 * x + lane, r = y / ZC, c = y % ZC;
+          const int tr = __shfl_sync(0xffffffffu, row, r);
+          size_t off = 0;
+          if (tr >= 0)
+            off = ((size_t)(tr >> a.logS) * a.S * RV +
+                   split_off(tr & (a.S - 1), 8 * c, a.S, RV, a.zsplit)) * 2;
+          cp_async16_or_zero(dst + tc_off(32 * w + r, c), a.Z + off, tr >= 0);
+        }
+      };
+      // groups in flight: K_0, Z_0, K_1, Z_1, ...; a tile's arrival follows
+      // the next copy's issue
+      int row = n > 0 ? tile_row(tc_tile(it, i0) * 128 + lt) : -1;
+      for (int i = 0; i < n; ++i) {
+        const int next =
+            i + 1 < n ? tile_row(tc_tile(it, i0 + i + 1) * 128 + lt) : -1;
+        if (i >= NST &&
+            !mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
+          break;
+        copy_k(i, row);
+        cp_async_commit();
+        if (i > 0) {
+          cp_async_wait_group<1>();
+          fence_proxy_async();
+          mbar_arrive(&zfull[(i - 1) % NST]);
+        }
+        if (i >= NST &&
+            !mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
+          break;
+        copy_z(i, row);
+        cp_async_commit();
+        cp_async_wait_group<1>();
+        fence_proxy_async();
+        mbar_arrive(&kfull[i % NST]);
+        row = next;
+      }
+      cp_async_wait_all();
+      fence_proxy_async();
+      if (n > 0 && !*abrt) mbar_arrive(&zfull[(n - 1) % NST]);
+    } else {
+      // A thread widens one row of each tile; the next part's bytes are
+      // requested before the current one is converted.
+      constexpr int KW = FMT == kSpanQ4 ? D / 8 : D / 4;    // 32-bit words of codes a row
+      constexpr int ZW = FMT == kSpanQ4 ? RV / 8 : RV / 4;
+      constexpr int KS = D / 64, ZS = (RV / 16 + 3) / 4;    // words of scales (4 bits only)
+      uint32_t kw[KW], zw[ZW], ks[KS > 0 ? KS : 1], zs[ZS];
+      auto load = [&](const uint8_t* base, int row, int wdt, uint32_t* dst, int nw, uint32_t* sc,
+                      bool z) {
+        if (row < 0) return;
+        if constexpr (FMT == kSpanQ4) {
+          const int tile = row >> a.logS, r = row & (a.S - 1);
+          const uint8_t* tp = base + (size_t)tile * q4_tile_bytes(a.S, wdt);
+          const uint8_t* cp = tp + r * (wdt / 2);
+#pragma unroll
+          for (int x = 0; x < nw; x += 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(cp + 4 * x));
+            dst[x] = v.x, dst[x + 1] = v.y, dst[x + 2] = v.z, dst[x + 3] = v.w;
+          }
+          const uint8_t* sp = tp + a.S * (wdt / 2) + r * (wdt / 16);
+          // rows of 2 (w 32) to 8 scale bytes, 2-byte aligned
+#pragma unroll
+          for (int x = 0; x < wdt / 16; x += 2) {
+            const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(sp + x));
+            if (x % 4 == 0)
+              sc[x / 4] = h;
+            else
+              sc[x / 4] |= h << 16;
+          }
+        } else {
+          const size_t tile = row >> a.logS;
+          const int r = row & (a.S - 1);
+#pragma unroll
+          for (int x = 0; x < nw; x += 4) {
+            const size_t off = z ? tile * a.S * wdt + split_off(r, 4 * x, a.S, wdt, a.zsplit)
+                                 : (size_t)row * wdt + 4 * x;
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(base + off));
+            dst[x] = v.x, dst[x + 1] = v.y, dst[x + 2] = v.z, dst[x + 3] = v.w;
+          }
+        }
+      };
+      auto put = [&](uint32_t dst, bool there, const uint32_t* src, int wdt, const uint32_t* sc) {
+#pragma unroll
+        for (int c = 0; c < wdt / 8; ++c) {  // 8 columns, 16 bytes of f16
+          uint32_t o[4] = {0u, 0u, 0u, 0u};
+          if (there) {
+            if constexpr (FMT == kSpanQ4) {
+              const uint32_t s = q4_scale_x2(sc[c / 8] >> (8 * ((c / 2) & 3)) & 255u);
+              q4_unpack8(src[c], o);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[k] = hmul2(o[k], s);
+            } else {
+              e4m3x4_to_f16(src[2 * c], o[0], o[1]);
+              e4m3x4_to_f16(src[2 * c + 1], o[2], o[3]);
+            }
+          }
+          sts128(dst + tc_off(lt, c), o[0], o[1], o[2], o[3]);
+        }
+      };
+      int row = n > 0 ? tile_row(tc_tile(it, i0) * 128 + lt) : -1;
+      if (n > 0) load(a.K, row, D, kw, KW, ks, false);
+      for (int i = 0; i < n; ++i) {
+        load(a.Z, row, RV, zw, ZW, zs, true);
+        const int next = i + 1 < n ? tile_row(tc_tile(it, i0 + i + 1) * 128 + lt) : -1;
+        if (i >= NST &&
+            !mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
+          break;
+        put(sk + (i % NST) * Gm::kKBytes, row >= 0, kw, D, ks);
+        fence_proxy_async();
+        mbar_arrive(&kfull[i % NST]);
+        if (i + 1 < n) load(a.K, next, D, kw, KW, ks, false);
+        if (i >= NST &&
+            !mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
+          break;
+        put(sz + (i % NST) * Gm::kZBytes, row >= 0, zw, RV, zs);
+        fence_proxy_async();
+        mbar_arrive(&zfull[i % NST]);
+        row = next;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int t = warp >> 2, r = tid & 127, row = t * 128 + r;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
+    if (t < nt) {
+      const int j = row / a.G, h = row - j * a.G;
+      const bool live = row < rows;
+      const int pos = live ? it.pos0 + j : -1;
+      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      // the row tile's first and last positions
+      const int pos_a = it.pos0 + t * tq, pos_b = min(it.pos0 + (t + 1) * tq, it.live_end) - 1;
+      const int lo_b = a.window > 0 ? max(0, pos_b - a.window + 1) : 0;
+      const float sl = a.scale_log2 * row_scale[row];
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int i = 0; i < n; ++i) {
+        ok = mbar_wait_or_abort(&sfull[t], i & 1, a.status, abrt);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const int t0 = tc_tile(it, i0 + i) * 128;
+        const bool masked = !(t0 + 127 <= pos_a && (t0 >= lo_b || t0 + 127 < a.sink));
+        // column x holds token t0 + x: visible up to pos, from lo on or below
+        // the sinks' end
+        const int me = pos - t0, mf = lo - t0, mg = a.sink - t0;
+        auto mask32 = [&](uint32_t (&s)[32], int x0) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (x0 + x > me || (x0 + x < mf && x0 + x >= mg)) s[x] = 0xff800000u;
+        };
+        uint32_t sa[32], sb[32];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 128; x += 64) {
+          tc_ld32(ts + x, sa);
+          tc_ld32(ts + x + 32, sb);
+          tc_wait_ld();
+          if (masked) {
+            mask32(sa, x);
+            mask32(sb, x + 32);
+          }
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            mx = fmaxf(mx, fmaxf(__uint_as_float(sa[y]), __uint_as_float(sb[y])));
+        }
+        mx *= sl;
+        if (i == 0) {
+          m = mx;
+        } else {
+          const bool grow = mx > m + kTcSlack;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(m - mx) : 1.f;
+            if (grow) m = mx;
+            l *= f;
+            ok = mbar_wait_or_abort(&ofull[t], (i - 1) & 1, a.status, abrt);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int x = 0; x < RV / 32; ++x) {
+              uint32_t o[32];
+              tc_ld32(to + 32 * x, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tc_st32(to + 32 * x, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum0 = 0.f, sum1 = 0.f;
+        // The scores are read a second time rather than held (128 registers a
+        // thread).  P of columns x .. x + 31 goes over columns x / 2 .. of S,
+        // which were read before.
+        auto weights = [&](uint32_t (&s)[32], int x) {
+          if (masked) mask32(s, x);
+          uint32_t p[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(s[y]), sl, -base));
+            const float p1 = ex2(fmaf(__uint_as_float(s[y + 1]), sl, -base));
+            sum0 += p0;
+            sum1 += p1;
+            if constexpr (BF) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+              p[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
+            } else {
+              const __half2 v = __floats2half2_rn(p0, p1);
+              p[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          }
+          tc_st16(ts + x / 2, p);
+        };
+        tc_ld32(ts, sa);
+        tc_wait_ld();
+        tc_ld32(ts + 32, sb);
+        weights(sa, 0);
+        tc_wait_ld();
+        tc_ld32(ts + 64, sa);
+        weights(sb, 32);
+        tc_wait_ld();
+        tc_ld32(ts + 96, sb);
+        weights(sa, 64);
+        tc_wait_ld();
+        weights(sb, 96);
+        l += sum0 + sum1;
+        tc_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&pfull[t]);
+      }
+      if (n > 0 && __all_sync(0xffffffffu, ok))
+        ok = mbar_wait_or_abort(&ofull[t], (n - 1) & 1, a.status, abrt);
+      if (__all_sync(0xffffffffu, ok)) {
+        tc_fence_after_sync();
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const size_t slot = blockIdx.x;
+        float* po = a.partial + (slot * kTcRows + row) * RV;
+        float* pm = a.partial + ((size_t)gridDim.x * kTcRows * RV) + (slot * kTcRows + row) * 2;
+        uint16_t* out =
+            a.out + (((size_t)it.b * a.n_tot + it.j0 + j) * a.Hq + it.g * a.G + h) * RV;
+#pragma unroll
+        for (int x = 0; x < RV / 32; ++x) {
+          uint32_t o[32];
+          if (n > 0) {
+            tc_ld32(to + 32 * x, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = 0u;
+          }
+          if (live && nsplit == 1) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 u =
+                    __floats2bfloat162_rn(__uint_as_float(o[y + 2 * k]) * inv,
+                                          __uint_as_float(o[y + 2 * k + 1]) * inv);
+                v[k] = *reinterpret_cast<const uint32_t*>(&u);
+              }
+              *reinterpret_cast<uint4*>(out + 32 * x + y) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4)
+              *reinterpret_cast<uint4*>(po + 32 * x + y) =
+                  make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+          }
+        }
+        if (live && nsplit > 1) {
+          pm[0] = m;
+          pm[1] = l;
+        }
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+}
+
+// Joins the nsplit partial sums of every row: a thread 4 columns.
+template <int RV>
+__global__ void __launch_bounds__(256) span_tc_merge_kernel(SpanArgs a, int nsplit, int items) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const TcItem it = tc_item(a, blockIdx.x);
+  const int rows = min(kTcRows, (a.n_tot - it.j0) * a.G);
+  const float* ml = a.partial + (size_t)items * nsplit * kTcRows * RV;
+  for (int o = blockIdx.y * 256 + threadIdx.x; o < rows * (RV / 4); o += gridDim.y * 256) {
+    const int row = o / (RV / 4), c = (o - row * (RV / 4)) * 4;
+    float M = -INFINITY, L = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < nsplit; ++s) {
+      const size_t slot = ((size_t)blockIdx.x * nsplit + s) * kTcRows + row;
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(ml + slot * 2));
+      if (v.x == -INFINITY) continue;
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.partial + slot * RV + c));
+      const float mn = fmaxf(M, v.x);
+      const float f0 = M == -INFINITY ? 0.f : ex2(M - mn), f1 = ex2(v.x - mn);
+      L = fmaf(L, f0, v.y * f1);
+      A.x = fmaf(A.x, f0, x.x * f1);
+      A.y = fmaf(A.y, f0, x.y * f1);
+      A.z = fmaf(A.z, f0, x.z * f1);
+      A.w = fmaf(A.w, f0, x.w * f1);
+      M = mn;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int j = row / a.G, h = row - j * a.G;
+    const __nv_bfloat162 u = __floats2bfloat162_rn(A.x * inv, A.y * inv);
+    const __nv_bfloat162 w = __floats2bfloat162_rn(A.z * inv, A.w * inv);
+    *reinterpret_cast<uint2*>(
+        a.out + (((size_t)it.b * a.n_tot + it.j0 + j) * a.Hq + it.g * a.G + h) * RV + c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
+  }
+}
+
+template <int FMT, int D, int RV>
+cudaError_t launch_span_tc_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
+  const int items = span_tc_items(a.B, a.Hkv, a.G, a.n_tot);
+  const int nsplit = span_tc_splits(items, a.n_tot, a.max_seq_len, a.sink, a.window);
+  cudaError_t e = cudaFuncSetAttribute(span_tc_kernel<FMT, D, RV>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)TcGeom<D, RV>::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_k(span_tc_kernel<FMT, D, RV>, dim3(items * nsplit), dim3(kTcThreads),
+               TcGeom<D, RV>::kSmem, st, pdl, a, nsplit);
+  if (e != cudaSuccess || nsplit == 1) return e;
+  const int rows = a.n_tot * a.G < kTcRows ? a.n_tot * a.G : kTcRows;
+  return launch_k(span_tc_merge_kernel<RV>, dim3(items, (rows * (RV / 4) + 255) / 256), dim3(256),
+                  0, st, pdl, a, nsplit, items);
+}
+
+template <int FMT>
+cudaError_t launch_span_tc_fmt(const SpanArgs& a, cudaStream_t st, bool pdl) {
+#define BKV_SPAN_TC_RV(DD)                                          \
+  switch (a.r_v) {                                                  \
+    case 32: return launch_span_tc_t<FMT, DD, 32>(a, st, pdl);      \
+    case 64: return launch_span_tc_t<FMT, DD, 64>(a, st, pdl);      \
+    case 96: return launch_span_tc_t<FMT, DD, 96>(a, st, pdl);      \
+    default: return launch_span_tc_t<FMT, DD, 128>(a, st, pdl);     \
+  }
+  if (a.d == 64) {
+    BKV_SPAN_TC_RV(64)
+  } else {
+    BKV_SPAN_TC_RV(128)
+  }
+#undef BKV_SPAN_TC_RV
+}
+
+}  // namespace
+}  // namespace basiskv
