@@ -280,7 +280,7 @@ int basiskv_cache4_attend(const basiskv_dims* dims, const basiskv_bf16* q,
   SpanArgs a = span_args(dims, q, seq_lens, max_seq_len, block_table, K4, Z4, a_out, status);
   a.sel = sel;
   a.top_k = top_k;
-  a.n_tot = a.n_q = 1;
+  a.n_tot = 1;
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.partial);
   return status_of(launch_span_q4(a, static_cast<cudaStream_t>(stream), pdl_allowed()));
 }
@@ -320,7 +320,7 @@ int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n
   a.sink = m.sink;
   a.window = m.window;
   a.partial = static_cast<float*>(workspace);
-  a.n_tot = a.n_q = n_q;
+  a.n_tot = n_q;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool pdl = pdl_allowed();
   if (window_streams(dims, n_q))

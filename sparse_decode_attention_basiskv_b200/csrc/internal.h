@@ -264,9 +264,8 @@ struct Route4Args {
 cudaError_t launch_route4(const Route4Args& a, cudaStream_t st, bool pdl);
 
 // ----------------------------------------------- attention over token spans
-// Attention of the query rows j0 .. j0 + n_q - 1 (of n_tot per sequence, the
-// last of them at position seq_lens[b] - 1) over a sliding window with
-// sinks, or (sel set, n_tot = 1) over selected pages.
+// Attention of the last n_tot tokens of every sequence over a sliding window
+// with sinks, or (sel set, n_tot = 1) over selected pages.
 enum SpanFormat { kSpanBf16 = 0, kSpanE4m3 = 1, kSpanQ4 = 2 };
 struct SpanArgs {
   const uint16_t* q;  // [B][n_tot][Hq][d]
@@ -278,7 +277,7 @@ struct SpanArgs {
   float* partial;      // span_slots() * rows * (r_v + 2) floats
   uint16_t* out;       // [B][n_tot][Hq][r_v] bf16
   int B, Hq, Hkv, G, d, r_v, S, logS, max_pages, num_phys, max_seq_len, top_k;
-  int n_tot, j0, n_q;
+  int n_tot;  // query tokens per sequence, the last at position seq_lens[b] - 1
   int sink, window;  // window 0: everything
   int zsplit;
   float scale_log2;
@@ -293,7 +292,7 @@ cudaError_t launch_span_bf16(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_e4m3(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_q4(const SpanArgs& a, cudaStream_t st, bool pdl);
 
-// Prompt form (tensor cores; j0 = 0, n_q = n_tot, no selection): work items
+// Prompt form (tensor cores; no selection): work items
 // of two row tiles, each cut into nsplit runs of KV tiles while the items
 // alone would leave SMs idle.
 inline int span_tc_items(int B, int Hkv, int G, int n_tot) {

@@ -8,29 +8,39 @@
 // Rows: query token j and head h of KV head g make row j * G + h; up to 16
 // rows (the M of mma.m16n8k16) share every Key and latent that is read.
 // Bound by HBM: 2 (d + r_v) multiply-adds a row and (d + r_v) cached columns
-// a token.
+// a token; over 4-bit caches closely followed by the instructions that widen
+// the codes (a conversion and a multiplication for two columns).
 //
-// Split: the unit of work is 16 tokens.  All units of all (sequence, KV head)
-// items form one line in (b, g, unit) order, cut into equal contiguous runs,
-// one a CTA, so that ragged lengths load every SM alike; each CTA finds its
-// run from a scan of the sequences' lengths.  A CTA's 8 warps take every 8th
-// unit of an item, keep their own running maximum, sum and accumulators, and
-// meet in shared memory when the item's part of the run ends.  An item that
-// lies in one CTA is written there; the others leave one partial a CTA, which
-// span_merge_kernel joins (the second launch, scheduled early).
+// Split: the unit of work is 16 tokens (4-bit caches: 32).  All units of all
+// (sequence, KV head) items form one line in (b, g, unit) order, cut into
+// equal contiguous runs, one a CTA, so that ragged lengths load every SM
+// alike; each CTA finds its run from a scan of the sequences' lengths.  A
+// CTA's 8 warps take every 8th unit of the run, keep their own running
+// maximum, sum and accumulators, and meet in shared memory where the run
+// passes from one item to the next.  An item that lies in one CTA is written
+// there; the others leave one partial a CTA, which span_merge_kernel joins
+// (the second launch, scheduled early).
 //
-// Data path: each warp copies its units (cp.async, 16 bytes a lane) into its
-// own ring of shared memory, kStages - 1 units ahead, and no other warp waits
-// for it.  The Keys are the B operand of QK (columns = tokens, as stored), so
-// the scores arrive with a row's tokens in the layout of the A operand of PV
-// and need no transposition; the latents are PV's B operand.  With at most 8
-// rows the upper half of PV's A operand holds the rounding remainders of the
-// weights, so they count with 16 (bf16) or 22 (f16) significant bits at no
-// cost.
+// Data path: each warp brings its units into its own ring of shared memory,
+// kStages - 1 units ahead and across item borders; no other warp waits for
+// it.  E4M3 and 4-bit units are one or a few contiguous pieces: one lane
+// hands them to the copy engine (cp.async.bulk), which costs a few
+// instructions a unit where 16-byte copies by all lanes cost 40 (a gather of
+// 1152 + 576 byte tiles alone runs at 6.2 TB/s this way).  bf16 units are
+// copied 16 bytes a lane, swizzled for ldmatrix.  The Keys are the B operand
+// of QK (columns = tokens, as stored), so the scores arrive with a row's
+// tokens in the layout of the A operand of PV and need no transposition; the
+// latents are PV's B operand.
 //
 // The running maximum moves only when a score passes it by 8 (a factor of
 // 256 in the weights, far inside the range of f16): then the warp takes the
 // rows' maxima over their lanes and rescales; all other units cost one vote.
+//
+// Precision: scores and sums in fp32.  The weights of PV are rounded to f16
+// (2^-12 of each weight, an eighth of the output's own rounding) where the
+// operands are f16, and held as bf16 roundings plus bf16 remainders (16
+// significant bits, the remainders in the rows of A that at most 8 query rows
+// leave free) or, with more than 8 rows, as bf16 where they are bf16.
 //
 // Formats: bf16 (bf16 products), E4M3 and 4 bits (widened to f16, which is
 // exact; each row's query is brought to f16 by a power of two that puts its
@@ -50,37 +60,44 @@ constexpr int kSpThreads = kLineMaxSeqs;  // a thread scans a sequence's length
 constexpr int kSpWarps = kSpThreads / 32;
 constexpr float kSpSlack = 8.f;
 
+// Tokens of a unit.
+template <int FMT>
+constexpr int sp_unit() {
+  return FMT == kSpanQ4 ? 32 : 16;
+}
+
 // What one sequence contributes: its live length, and the units of one KV
 // head (n_sink units of sink tokens, then the window's from lo_unit on).
 struct SpanSeq {
   int T, n_sink, lo_unit, n;
 };
+template <int UT>
 __device__ __forceinline__ SpanSeq span_seq(const SpanArgs& a, int len) {
   SpanSeq s;
   s.T = len;
-  const int last = len - a.n_tot + a.j0 + a.n_q - 1;  // position of the last row
-  if (len <= 0 || len > a.max_seq_len || last < 0) {
+  const int last = len - 1;
+  if (len <= 0 || len > a.max_seq_len) {
     s.T = 0;
     s.n_sink = s.lo_unit = s.n = 0;
   } else if (a.sel) {
     s.n_sink = s.lo_unit = 0;
-    s.n = a.top_k << (a.logS - 4);
+    s.n = a.S >= UT ? a.top_k * (a.S / UT) : (a.top_k + 1) >> 1;
   } else {
-    const int p0 = max(0, last - a.n_q + 1);
-    const int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-    s.lo_unit = lo >> 4;
-    s.n_sink = min((a.sink + 15) >> 4, s.lo_unit);
-    s.n = s.n_sink + (last >> 4) - s.lo_unit + 1;
+    const int lo = a.window > 0 ? max(0, max(len - a.n_tot, 0) - a.window + 1) : 0;
+    s.lo_unit = lo / UT;
+    s.n_sink = min((a.sink + UT - 1) / UT, s.lo_unit);
+    s.n = s.n_sink + last / UT - s.lo_unit + 1;
   }
   return s;
 }
 
 // pre[b] = units of one KV head of the sequences before b; pre[B] = all.
+template <int UT>
 __device__ __forceinline__ void span_scan(const SpanArgs& a, long long* pre, bool report) {
   line_scan(a.B, pre, [&](int b) -> long long {
     const int len = a.seq_lens[b];
     if (report && (len < 0 || len > a.max_seq_len)) raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
-    return span_seq(a, len).n;
+    return span_seq<UT>(a, len).n;
   });
 }
 
@@ -96,22 +113,32 @@ __device__ __forceinline__ int span_cta_of(long long x, long long total, int C) 
   return (int)(c < C - 1 ? c : C - 1);
 }
 
-// Bytes of one unit (16 tokens) in a warp's ring.
+// Bytes of one unit in a warp's ring, and of the ring's part of shared memory.
 template <int FMT, int D, int RV>
 constexpr int sp_unit_bytes() {
-  return FMT == kSpanBf16 ? 32 * (D + RV) : (FMT == kSpanE4m3 ? 16 * (D + RV) : 9 * (D + RV));
+  return sp_unit<FMT>() * (D + RV) * (FMT == kSpanBf16 ? 32 : (FMT == kSpanE4m3 ? 16 : 9)) / 16;
 }
-// Ring depth: bf16 units are 3-8 KB and one CTA of 8 warps fills an SM's
-// shared memory; the narrower formats run two CTAs.
-template <int FMT>
+// CTAs an SM: two, except where the queries' and accumulators' registers (16
+// rows) or the ring (bf16) allow one.
+template <int FMT, int NR>
+constexpr int sp_ctas() {
+  return FMT == kSpanBf16 || NR == 2 ? 1 : 2;
+}
+template <int FMT, int D, int RV, int NR>
+constexpr size_t sp_meet_bytes() {
+  return (size_t)kSpWarps * 8 * NR * (RV + 2) * 4;
+}
+// Ring depth: 4 units, fewer where shared memory ends (2 at least).
+template <int FMT, int D, int RV, int NR>
 constexpr int sp_stages() {
-  return FMT == kSpanBf16 ? 3 : 4;
+  const size_t room = 224 * 1024 / sp_ctas<FMT, NR>() - 6 * 1024 - sp_meet_bytes<FMT, D, RV, NR>();
+  const size_t n = room / ((size_t)kSpWarps * sp_unit_bytes<FMT, D, RV>());
+  return n < 4 ? (int)n : 4;
 }
 template <int FMT, int D, int RV, int NR>
 constexpr size_t sp_smem() {
-  const size_t ring = (size_t)kSpWarps * sp_stages<FMT>() * sp_unit_bytes<FMT, D, RV>();
-  const size_t meet = (size_t)kSpWarps * 8 * NR * (RV + 2) * 4;
-  return ring > meet ? ring : meet;
+  return (size_t)kSpWarps * sp_stages<FMT, D, RV, NR>() * sp_unit_bytes<FMT, D, RV>() +
+         sp_meet_bytes<FMT, D, RV, NR>();
 }
 
 // The latent column that lane column n (0..7) of accumulator tile t holds:
@@ -123,45 +150,243 @@ __device__ __forceinline__ int sp_col(int t, int n) {
   if (t < 8 * (RV / 64)) return 64 * (t >> 3) + 8 * n + (t & 7);
   return 64 * (RV / 64) + 4 * n + (t & 3);
 }
+// Swizzled 16-byte chunk of a bf16 latent row in shared memory.
+template <int RV>
+__device__ __forceinline__ int sp_zchunk(int r, int ch) {
+  if (RV == 32) return ch ^ ((r >> 1) & 3);
+  if (RV == 96 && ch >= 8) return 8 + ((ch ^ (r >> 1)) & 3);
+  return ch ^ (r & 7);
+}
+
+__device__ __forceinline__ void mbar_arrive_only(uint32_t bar) {
+  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar)
+               : "memory");
+}
 
 template <int FMT, int D, int RV, int NR>
-__global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 2)
-    span_kernel(SpanArgs a) {
-  constexpr int NT = RV / 8, KS = D / 16, NST = sp_stages<FMT>();
+__global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(SpanArgs a) {
+  constexpr int UT = sp_unit<FMT>(), HT = UT / 2;  // tokens of a unit, of its halves
+  constexpr int TT = UT / 8;                       // 8-token column tiles of QK
+  constexpr int NT = RV / 8, KS = D / 16, NST = sp_stages<FMT, D, RV, NR>();
   constexpr int UB = sp_unit_bytes<FMT, D, RV>();
   constexpr int RS = RV + 2;
-  extern __shared__ __align__(16) uint8_t sp_smem_raw[];
+  constexpr bool BULK = FMT != kSpanBf16;
+  static_assert(NST >= 2 && (D + RV) * UT / 16 * 9 % 16 == 0, "");
+  extern __shared__ __align__(128) uint8_t sp_smem_raw[];
   __shared__ long long pre[257];
-  __shared__ uint32_t ring_t0[kSpWarps][NST];
+  __shared__ uint2 tags[kSpWarps][NST];      // a unit's halves: first tokens (~0: absent)
+  __shared__ uint64_t bars[kSpWarps * NST];  // a unit has landed
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(sp_smem_raw) + warp * NST * UB;
-  float* meet = reinterpret_cast<float*>(sp_smem_raw);  // [warp][row][RV + 2] after an item
-  const int R = a.n_q * a.G;
+  const uint32_t bar = smem_u32(bars + warp * NST);
+  // [warp][row][2 + RV] where the warps meet after an item
+  float* meet = reinterpret_cast<float*>(sp_smem_raw + kSpWarps * NST * UB);
+  const int R = a.n_tot * a.G;
 
+  if (BULK && tid < kSpWarps * NST) mbar_init(bars + tid, 1);
+  if (BULK) fence_barrier_init();
   pdl_wait();
   pdl_launch_dependents();
-  span_scan(a, pre, blockIdx.x == 0);
+  span_scan<UT>(a, pre, blockIdx.x == 0);
   const long long total = pre[a.B] * a.Hkv;
   const int C = span_ctas(total, gridDim.x);
   if ((int)blockIdx.x >= C) return;
-  const long long c_end = total * (blockIdx.x + 1) / C;
-  long long seg = total * blockIdx.x / C;
-  int b = seg < c_end ? line_find(a.B, pre, a.Hkv, seg) : 0;
-  while (seg < c_end) {
-    while (pre[b + 1] * a.Hkv <= seg) ++b;
-    const SpanSeq sq = span_seq(a, a.seq_lens[b]);
-    const int g = (int)((seg - pre[b] * a.Hkv) / sq.n);
-    const long long x0 = pre[b] * a.Hkv + (long long)g * sq.n;
-    const int u_begin = (int)(seg - x0);
-    const int u_end = (int)min((long long)sq.n, c_end - x0);
+  // the run [start, start + run) of the line; `start` stays in shared memory
+  __shared__ long long start;
+  int run;
+  {
+    const long long s0 = total * blockIdx.x / C;
+    run = (int)(total * (blockIdx.x + 1) / C - s0);
+    if (tid == 0) start = s0;
+  }
+  __syncthreads();
+  if (run <= 0) return;
+
+  // ---- the warp's units: warp + 8 k of the run, k < n_units, whatever their items
+  const int n_units = warp < run ? (run - warp + kSpWarps - 1) / kSpWarps : 0;
+  // Ids of 32 units ahead, one a lane: the first token of the unit's halves and
+  // their tile rows (physical page and KV head * S + row; -1: not there).
+  int id_ta = 0, id_tb = 0, id_ra = -1, id_rb = -1, id_base = 0;
+  auto fetch_ids = [&](int base) {
+    id_base = base;
+    id_ra = id_rb = -1;
+    const int k = base + lane;
+    if (k >= n_units) return;
+    const long long x = start + warp + (long long)kSpWarps * k;
+    const int b = line_find(a.B, pre, a.Hkv, x);
+    const SpanSeq sq = span_seq<UT>(a, a.seq_lens[b]);
+    const long long y = x - pre[b] * a.Hkv;
+    const int g = (int)(y / sq.n), u = (int)(y - (long long)g * sq.n);
+    const int lo = a.window > 0 ? max(0, max(sq.T - a.n_tot, 0) - a.window + 1) : 0;
+    auto tile_row = [&](int t) -> int {
+      // no row sees tokens between the sinks and the window: their pages are
+      // not looked up
+      if (t >= sq.T || (t + HT <= lo && t >= a.sink)) return -1;
+      const int p = t >> a.logS;
+      const int pp = p < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + p) : -1;
+      if (pp < 0 || pp >= a.num_phys) {
+        raise_status(a.status, BASISKV_DEV_BAD_PAGE);
+        return -1;
+      }
+      return ((pp * a.Hkv + g) << a.logS) + (t & (a.S - 1));
+    };
+    auto selected = [&](int e) -> int {  // first token of selected page e, -1: none
+      const int lp = e < a.top_k
+                         ? __ldg(a.sel + (size_t)(b * a.Hkv + g) * a.top_k + e) : -1;
+      if (lp >= a.max_pages) raise_status(a.status, BASISKV_DEV_BAD_PAGE);
+      return lp >= 0 && lp < a.max_pages ? lp << a.logS : -1;
+    };
+    if (a.sel) {
+      if (a.S >= UT) {
+        id_ta = selected(u);
+        id_tb = id_ta + HT;
+      } else {
+        id_ta = selected(2 * u);
+        id_tb = selected(2 * u + 1);
+      }
+      if (id_ta >= 0) id_ra = tile_row(id_ta);
+      if (a.S >= UT ? id_ta >= 0 : id_tb >= 0) id_rb = tile_row(id_tb);
+    } else {
+      id_ta = UT * (u < sq.n_sink ? u : sq.lo_unit + u - sq.n_sink);
+      id_tb = id_ta + HT;
+      id_ra = tile_row(id_ta);
+      id_rb = tile_row(id_tb);
+    }
+  };
+  // Requests unit k into ring slot `slot` (k grows by one from call to call).
+  auto issue = [&](int k, int slot) {
+    if (k < n_units) {
+      if (k - id_base >= 32) fetch_ids(k);
+      const uint32_t st = ring + slot * UB;
+      if constexpr (BULK) {
+        if (lane == k - id_base) {  // the lane that knows the unit
+          tags[warp][slot] = make_uint2(id_ra >= 0 ? (uint32_t)id_ta : ~0u,
+                                        id_rb >= 0 ? (uint32_t)id_tb : ~0u);
+          const uint32_t b = bar + 8 * slot;
+          auto copy = [&](uint32_t dst, const uint8_t* src, uint32_t bytes) {
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], "
+                "%2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(b)
+                : "memory");
+          };
+          auto expect = [&](uint32_t bytes) {
+            asm volatile(
+                "{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(b),
+                "r"(bytes)
+                : "memory");
+          };
+          const int present = (id_ra >= 0) + (id_rb >= 0);
+          if (!present) {
+            mbar_arrive_only(b);
+          } else if constexpr (FMT == kSpanQ4) {
+            if (a.S >= UT) {  // the unit is one tile: codes and scales of 32 rows
+              const size_t tile = (id_ra >= 0 ? id_ra : id_rb - HT) >> a.logS;
+              expect(UB);
+              copy(st, a.K + tile * (2 * 9 * D), 2 * 9 * D);
+              copy(st + 2 * 9 * D, a.Z + tile * (2 * 9 * RV), 2 * 9 * RV);
+            } else {  // two tiles of 16 rows, one behind the other
+              expect(present * (UB / 2));
+              if (id_ra >= 0) {
+                copy(st, a.K + (size_t)(id_ra >> a.logS) * (9 * D), 9 * D);
+                copy(st + 2 * 9 * D, a.Z + (size_t)(id_ra >> a.logS) * (9 * RV), 9 * RV);
+              }
+              if (id_rb >= 0) {
+                copy(st + 9 * D, a.K + (size_t)(id_rb >> a.logS) * (9 * D), 9 * D);
+                copy(st + 2 * 9 * D + 9 * RV, a.Z + (size_t)(id_rb >> a.logS) * (9 * RV), 9 * RV);
+              }
+            }
+          } else {  // E4M3 rows; latents [rows][F] and then [rows][RV - F]
+            const int F = a.zsplit;
+            expect(present * HT * (D + RV));
+            auto half = [&](int row, int at, int rows) {
+              copy(st + at * D, a.K + (size_t)row * D, rows * D);
+              const uint8_t* tile = a.Z + (size_t)(row >> a.logS) * a.S * RV;
+              const int r = row & (a.S - 1);
+              copy(st + 16 * D + at * F, tile + r * F, rows * F);
+              if (F < RV)
+                copy(st + 16 * D + 16 * F + at * (RV - F), tile + a.S * F + r * (RV - F),
+                     rows * (RV - F));
+            };
+            if (a.S >= UT && present == 2) {
+              half(id_ra, 0, UT);
+            } else {
+              if (id_ra >= 0) half(id_ra, 0, HT);
+              if (id_rb >= 0) half(id_rb, HT, HT);
+            }
+          }
+        }
+      } else {
+        const int src = k - id_base;
+        const int ra = __shfl_sync(0xffffffffu, id_ra, src);
+        const int rb = __shfl_sync(0xffffffffu, id_rb, src);
+        if (lane == src)
+          tags[warp][slot] = make_uint2(id_ra >= 0 ? (uint32_t)id_ta : ~0u,
+                                        id_rb >= 0 ? (uint32_t)id_tb : ~0u);
+        constexpr int KC = D / 8, ZC = RV / 8;
+#pragma unroll
+        for (int x = 0; x < 16 * KC; x += 32) {
+          const int i = x + lane, r = i / KC, ch = i % KC;
+          const int tr = r < HT ? ra + r : rb + r - HT;
+          if (r < HT ? ra >= 0 : rb >= 0)
+            cp_async16_or_zero(st + (r * KC + (ch ^ (r & 7))) * 16,
+                               a.K + ((size_t)tr * D + ch * 8) * 2);
+        }
+#pragma unroll
+        for (int x = 0; x < 16 * ZC; x += 32) {
+          const int i = x + lane, r = i / ZC, ch = i % ZC;
+          const int tr = r < HT ? ra + r : rb + r - HT;
+          if (r < HT ? ra >= 0 : rb >= 0)
+            cp_async16_or_zero(
+                st + 32 * D + (r * ZC + sp_zchunk<RV>(r, ch)) * 16,
+                a.Z + ((size_t)(tr >> a.logS) * a.S * RV +
+                       split_off(tr & (a.S - 1), ch * 8, a.S, RV, a.zsplit)) * 2);
+        }
+      }
+    }
+    if constexpr (!BULK) cp_async_commit();
+  };
+
+  int k_next = 0, slot_next = 0;  // the next unit to request, and its slot
+  auto request = [&]() {
+    issue(k_next++, slot_next);
+    slot_next = slot_next + 1 == NST ? 0 : slot_next + 1;
+  };
+  if (n_units > 0) fetch_ids(0);
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) request();
+  int slot = 0;
+  uint32_t phase = 0;  // of the slots' barriers in this turn of the ring
+
+  // Byte offsets within a unit that depend on the page size (4 bits only): the
+  // second half's codes and the scales.
+  const bool one_tile = a.S >= UT;
+  const uint32_t kc1 = one_tile ? 8 * D : 9 * D, ks0 = one_tile ? 16 * D : 8 * D,
+                 ks1 = one_tile ? 17 * D : 17 * D;
+  const uint32_t zc1 = one_tile ? 8 * RV : 9 * RV, zs0 = one_tile ? 16 * RV : 8 * RV,
+                 zs1 = one_tile ? 17 * RV : 17 * RV;
+
+  int seg = 0;  // the run's next unit
+  while (seg < run) {
+    int b, g, count, item_end;
+    bool alone;  // the whole item is in this run
+    SpanSeq sq;
+    {
+      const long long x = start + seg;
+      b = line_find(a.B, pre, a.Hkv, x);
+      sq = span_seq<UT>(a, a.seq_lens[b]);
+      const long long y = x - pre[b] * a.Hkv;
+      g = (int)(y / sq.n);
+      const int u = (int)(y - (long long)g * sq.n);  // the item's unit at seg
+      item_end = min(run, seg + sq.n - u);
+      alone = u == 0 && item_end == seg + sq.n;
+      // the run's warps take turns from its start on, whatever the item
+      const int w0 = seg + ((warp - seg) & (kSpWarps - 1));
+      count = w0 < item_end ? (item_end - w0 + kSpWarps - 1) / kSpWarps : 0;
+    }
     const int bg = b * a.Hkv + g;
-    const int T = sq.T;
-    // row positions: query token j sits at pos0 + j
-    const int pos0 = T - a.n_tot + a.j0;
-    const int p_last = pos0 + a.n_q - 1;
+    const int pos0 = sq.T - a.n_tot, p_last = sq.T - 1;  // the rows' positions
     const int lo_first = a.window > 0 ? max(0, max(pos0, 0) - a.window + 1) : 0;
     const int lo_last = a.window > 0 ? max(0, p_last - a.window + 1) : 0;
-    const int live_end = p_last + 1;  // no row sees a token from here on
 
     // ---- queries: rows n and n + 8
     int pos[NR], lo[NR];
@@ -175,7 +400,7 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
       pos[i] = ok ? pos0 + j : -1;
       lo[i] = a.window > 0 ? max(0, pos[i] - a.window + 1) : 0;
       const uint16_t* qr =
-          a.q + (((size_t)b * a.n_tot + a.j0 + (ok ? j : 0)) * a.Hq + g * a.G + (ok ? h : 0)) * D;
+          a.q + (((size_t)b * a.n_tot + (ok ? j : 0)) * a.Hq + g * a.G + (ok ? h : 0)) * D;
       sl[i] = a.scale_log2;
       if constexpr (FMT == kSpanBf16) {
 #pragma unroll
@@ -186,7 +411,7 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
                              : 0u;
       } else {
         // k-step k of the lane's columns: 4 consecutive ones (2 pairs)
-        float m = 0.f;
+        float mq = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const int col = FMT == kSpanE4m3 ? 64 * (k >> 2) + 16 * c + 4 * (k & 3)
@@ -197,12 +422,12 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 f = bf16x2_to_f2(qa[k][i][e]);
-            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            mq = fmaxf(mq, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int ex = m > 0.f ? (int)((__float_as_uint(m) >> 23) & 0xffu) - 126 : 15;
+        mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
+        mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
+        const int ex = mq > 0.f ? (int)((__float_as_uint(mq) >> 23) & 0xffu) - 126 : 15;
         const int sh = max(-126, min(126, 15 - ex));
         const float sc = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll
@@ -217,145 +442,40 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
       }
     }
 
-    float m[NR], l[NR], acc[NT][4];
+    // m: the rows' reference (log2 units); thr: the raw score that moves it
+    float m[NR], thr[NR], l[NR], acc[NT][4];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    for (int i = 0; i < NR; ++i) m[i] = thr[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
 
-    // ---- the warp's units: u_begin + warp + 8 i
-    const int u_first = u_begin + warp;
-    const int count = u_first < u_end ? (u_end - u_first + kSpWarps - 1) / kSpWarps : 0;
-    // Ids of 32 units ahead, one a lane: the first token, and the tile row of
-    // tokens 0-7 and 8-15 of the unit (-1: nothing to read there).
-    int id_t0 = 0, id_ra = -1, id_rb = -1, id_base = 0;
-    auto tile_row = [&](int t) -> int {
-      if (t >= live_end) return -1;
-      const int p = t >> a.logS;
-      const int pp = p < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + p) : -1;
-      if (pp < 0 || pp >= a.num_phys) {
-        raise_status(a.status, BASISKV_DEV_BAD_PAGE);
-        return -1;
-      }
-      return ((pp * a.Hkv + g) << a.logS) + (t & (a.S - 1));
-    };
-    auto fetch_ids = [&](int base) {
-      id_base = base;
-      const int i = base + lane;
-      id_ra = id_rb = -1;
-      id_t0 = 0;
-      if (i >= count) return;
-      const int u = u_first + kSpWarps * i;
-      if (a.sel) {
-        const int lp = __ldg(a.sel + (size_t)bg * a.top_k + (u >> (a.logS - 4)));
-        if (lp < 0) return;
-        if (lp >= a.max_pages) {
-          raise_status(a.status, BASISKV_DEV_BAD_PAGE);
-          return;
-        }
-        id_t0 = (lp << a.logS) + 16 * (u & ((a.S >> 4) - 1));
-      } else {
-        id_t0 = 16 * (u < sq.n_sink ? u : sq.lo_unit + u - sq.n_sink);
-      }
-      id_ra = tile_row(id_t0);
-      if (a.S >= 16)
-        id_rb = id_ra < 0 || id_t0 + 8 >= live_end ? -1 : id_ra + 8;
-      else
-        id_rb = tile_row(id_t0 + 8);
-    };
-    // Whether some row of this launch sees token t.
-    auto seen = [&](int t) { return t < live_end && (t >= lo_first || t < a.sink); };
-
-    auto issue = [&](int i) {
-      if (i < count) {
-        if (i - id_base >= 32) fetch_ids(i);
-        const int src = i - id_base;
-        const int t0 = __shfl_sync(0xffffffffu, id_t0, src);
-        const int ra = __shfl_sync(0xffffffffu, id_ra, src);
-        const int rb = __shfl_sync(0xffffffffu, id_rb, src);
-        const int slot = i % NST;
-        const uint32_t st = ring + slot * UB;
-        // positions have 30 bits; above them, which halves are there
-        if (lane == 0)
-          ring_t0[warp][slot] =
-              (uint32_t)t0 | (ra >= 0 ? 1u << 30 : 0u) | (rb >= 0 ? 1u << 31 : 0u);
-        if (ra >= 0 || rb >= 0) {
-          if constexpr (FMT == kSpanQ4) {
-            // codes and scales of 16 rows, contiguous each
-            const int tile = ra >> a.logS, row = ra & (a.S - 1);
-            const uint8_t* kt = a.K + (size_t)tile * q4_tile_bytes(a.S, D);
-            const uint8_t* zt = a.Z + (size_t)tile * q4_tile_bytes(a.S, RV);
-#pragma unroll
-            for (int x = 0; x < D / 2; x += 32)
-              cp_async16_or_zero(st + 16 * (x + lane), kt + row * (D / 2) + 16 * (x + lane), true);
-#pragma unroll
-            for (int x = 0; x < RV / 2; x += 32)
-              if (RV / 2 - x >= 32 || lane < RV / 2 - x)
-                cp_async16_or_zero(st + 9 * D + 16 * (x + lane),
-                                   zt + row * (RV / 2) + 16 * (x + lane), true);
-            if (lane < D / 16)
-              cp_async16_or_zero(st + 8 * D + 16 * lane,
-                                 kt + a.S * (D / 2) + row * (D / 16) + 16 * lane, true);
-            else if (lane < D / 16 + RV / 16)
-              cp_async16_or_zero(st + 9 * D + 8 * RV + 16 * (lane - D / 16),
-                                 zt + a.S * (RV / 2) + row * (RV / 16) + 16 * (lane - D / 16),
-                                 true);
-          } else {
-            constexpr int EB = FMT == kSpanBf16 ? 2 : 1;  // bytes a column
-            constexpr int KC = D * EB / 16, ZC = RV * EB / 16;
-            const bool whole = t0 + 15 < live_end && (t0 >= lo_first || t0 + 15 < a.sink);
-#pragma unroll
-            for (int x = 0; x < 16 * KC; x += 32) {
-              const int i2 = x + lane, r = i2 / KC, ch = i2 % KC;
-              const int tr = r < 8 ? ra + r : rb + r - 8;
-              const bool ok = (r < 8 ? ra >= 0 : rb >= 0) && (whole || seen(t0 + r));
-              // chunks of a row are rotated within shared memory so that the
-              // lanes' reads fall into different banks
-              const int sw = FMT == kSpanBf16 ? ch ^ (r & 7) : (D == 128 ? ch ^ ((r & 1) << 2) : ch);
-              cp_async16_or_zero(st + (r * KC + sw) * 16,
-                                 a.K + (ok ? ((size_t)tr * D * EB + ch * 16) : 0), ok);
-            }
-#pragma unroll
-            for (int x = 0; x < 16 * ZC; x += 32) {
-              const int i2 = x + lane, r = i2 / ZC, ch = i2 % ZC;
-              const int tr = r < 8 ? ra + r : rb + r - 8;
-              const bool ok = (r < 8 ? ra >= 0 : rb >= 0) && (whole || seen(t0 + r));
-              size_t off = 0;
-              if (ok) {
-                const int tile = tr >> a.logS, row = tr & (a.S - 1);
-                off = ((size_t)tile * a.S * RV +
-                       split_off(row, ch * (16 / EB), a.S, RV, a.zsplit)) * EB;
-              }
-              const int sw = FMT == kSpanBf16 ? (RV == 32 ? ch ^ ((r >> 1) & 3) :
-                                                 RV == 96 ? (ch < 8 ? ch ^ (r & 7)
-                                                                    : 8 + ((ch ^ (r >> 1)) & 3))
-                                                          : ch ^ (r & 7))
-                                              : ch;
-              cp_async16_or_zero(st + 16 * D * EB + (r * ZC + sw) * 16, a.Z + off, ok);
-            }
-          }
-        }
-      }
-      cp_async_commit();
-    };
-
-    if (count > 0) fetch_ids(0);
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i) issue(i);
     for (int it = 0; it < count; ++it) {
       __syncwarp();  // every lane is done with the slot that is filled next
-      issue(it + NST - 1);
-      cp_async_wait_group<NST - 1>();
-      __syncwarp();  // the unit's copies by all lanes have landed
-      const int slot = it % NST;
-      const uint32_t tag = ring_t0[warp][slot];
-      if (tag < 1u << 30) continue;  // nothing to read there
-      const int t0 = (int)(tag & 0x3fffffffu);
-      const uint32_t ks = ring + slot * UB;
-      constexpr int ZB = FMT == kSpanBf16 ? 32 * D : (FMT == kSpanE4m3 ? 16 * D : 9 * D);
-      const uint32_t zs = ks + ZB;
-      // ---- scores: s[e] of rows n (and n + 8), tokens 2c, 2c + 1 (tile 0), + 8 (tile 1)
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      request();
+      if constexpr (BULK) {
+        mbar_wait(bars + warp * NST + slot, phase, a.status);
+      } else {
+        cp_async_wait_group<NST - 1>();
+        __syncwarp();
+      }
+      const uint2 tag = tags[warp][slot];
+      const uint32_t ks = ring + slot * UB, zs = ks + UT * D * (FMT == kSpanBf16 ? 32 : FMT == kSpanE4m3 ? 16 : 9) / 16;
+      if (++slot == NST) {
+        slot = 0;
+        phase ^= 1;
+      }
+      if ((tag.x & tag.y) == ~0u) continue;  // nothing there
+      // ---- scores: s[t][e] of rows n (e < 2) and n + 8, tokens 8 t + 2c, + 1
+      float s[TT][4];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      auto qk = [&](int t, int k, uint32_t b0, uint32_t b1) {
+        const uint32_t a1 = NR == 2 ? qa[k][NR - 1][0] : 0u, a3 = NR == 2 ? qa[k][NR - 1][1] : 0u;
+        if constexpr (FMT == kSpanBf16)
+          mma_bf16_16816(s[t], qa[k][0][0], a1, qa[k][0][1], a3, b0, b1);
+        else
+          mma_f16_16816(s[t], qa[k][0][0], a1, qa[k][0][1], a3, b0, b1);
+      };
       if constexpr (FMT == kSpanBf16) {
         const int mi = lane >> 3, row = (lane & 7) + 8 * (mi >> 1);
 #pragma unroll
@@ -363,96 +483,91 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
           const int ch = (2 * k + (mi & 1)) ^ (row & 7);
           uint32_t b0, b1, b2, b3;
           ldmatrix_x4(ks + row * (2 * D) + ch * 16, b0, b1, b2, b3);
-          mma_bf16_16816(s0, qa[k][0][0], NR == 2 ? qa[k][NR - 1][0] : 0u, qa[k][0][1],
-                         NR == 2 ? qa[k][NR - 1][1] : 0u, b0, b1);
-          mma_bf16_16816(s1, qa[k][0][0], NR == 2 ? qa[k][NR - 1][0] : 0u, qa[k][0][1],
-                         NR == 2 ? qa[k][NR - 1][1] : 0u, b2, b3);
+          qk(0, k, b0, b1);
+          qk(1, k, b2, b3);
         }
       } else if constexpr (FMT == kSpanE4m3) {
 #pragma unroll
-        for (int k4 = 0; k4 < KS / 4; ++k4) {
-          // 16 columns of tokens n and n + 8
-          const int ch = c + 4 * k4;
-          const uint4 x = lds128(ks + n * D + (D == 128 ? ch ^ ((n & 1) << 2) : ch) * 16);
-          const uint4 y = lds128(ks + (n + 8) * D + (D == 128 ? ch ^ ((n & 1) << 2) : ch) * 16);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        for (int k4 = 0; k4 < KS / 4; ++k4)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t b0, b1, b2, b3;
-            e4m3x4_to_f16(xw[w], b0, b1);
-            e4m3x4_to_f16(yw[w], b2, b3);
-            const int k = 4 * k4 + w;
-            mma_f16_16816(s0, qa[k][0][0], NR == 2 ? qa[k][NR - 1][0] : 0u, qa[k][0][1],
-                          NR == 2 ? qa[k][NR - 1][1] : 0u, b0, b1);
-            mma_f16_16816(s1, qa[k][0][0], NR == 2 ? qa[k][NR - 1][0] : 0u, qa[k][0][1],
-                          NR == 2 ? qa[k][NR - 1][1] : 0u, b2, b3);
+          for (int t = 0; t < TT; ++t) {
+            // 16 columns of token 8 t + n
+            const uint4 x = lds128(ks + (n + 8 * t) * D + (c + 4 * k4) * 16);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16(xw[w], b0, b1);
+              qk(t, 4 * k4 + w, b0, b1);
+            }
           }
-        }
       } else {
-        // D / 4 columns of tokens n and n + 8: D / 8 bytes, one scale per 16
-        uint32_t xw[D / 32], yw[D / 32], sx[D / 64], sy[D / 64];
-        if constexpr (D == 128) {
-          const uint4 x = lds128(ks + n * 64 + 16 * c), y = lds128(ks + (n + 8) * 64 + 16 * c);
-          xw[0] = x.x, xw[1] = x.y, xw[2] = x.z, xw[3] = x.w;
-          yw[0] = y.x, yw[1] = y.y, yw[2] = y.z, yw[3] = y.w;
-          const uint32_t u = lds16(ks + 8 * D + n * 8 + 2 * c);
-          const uint32_t v = lds16(ks + 8 * D + (n + 8) * 8 + 2 * c);
-          sx[0] = q4_scale_x2(u & 255u), sx[D / 64 - 1] = q4_scale_x2(u >> 8);
-          sy[0] = q4_scale_x2(v & 255u), sy[D / 64 - 1] = q4_scale_x2(v >> 8);
-        } else {
-          const uint2 x = lds64(ks + n * 32 + 8 * c), y = lds64(ks + (n + 8) * 32 + 8 * c);
-          xw[0] = x.x, xw[1] = x.y;
-          yw[0] = y.x, yw[1] = y.y;
-          sx[0] = q4_scale_x2(lds8(ks + 8 * D + n * 4 + c));
-          sy[0] = q4_scale_x2(lds8(ks + 8 * D + (n + 8) * 4 + c));
-        }
+        // D / 4 columns of token 8 t + n: D / 8 bytes, one scale per 16
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          uint32_t x[4], y[4];
-          q4_unpack8(xw[w], x);
-          q4_unpack8(yw[w], y);
+        for (int t = 0; t < TT; ++t) {
+          const uint32_t row = ks + (t >= 2 ? kc1 : 0u) + (n + 8 * (t & 1)) * (D / 2);
+          const uint32_t scl = ks + (t >= 2 ? ks1 : ks0) + (n + 8 * (t & 1)) * (D / 16);
+          uint32_t xw[D / 32], sx[D / 64];
+          if constexpr (D == 128) {
+            const uint4 x = lds128(row + 16 * c);
+            xw[0] = x.x, xw[1] = x.y, xw[2] = x.z, xw[3] = x.w;
+            const uint32_t u = lds16(scl + 2 * c);
+            sx[0] = __byte_perm(u, 0u, 0x4040) << 7;
+            sx[D / 64 - 1] = __byte_perm(u, 0u, 0x4141) << 7;
+          } else {
+            const uint2 x = lds64(row + 8 * c);
+            xw[0] = x.x, xw[1] = x.y;
+            sx[0] = q4_scale_x2(lds8(scl + c));
+          }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = 2 * w + e;
-            mma_f16_16816(s0, qa[k][0][0], NR == 2 ? qa[k][NR - 1][0] : 0u, qa[k][0][1],
-                          NR == 2 ? qa[k][NR - 1][1] : 0u, hmul2(x[2 * e], sx[w / 2]),
-                          hmul2(x[2 * e + 1], sx[w / 2]));
-            mma_f16_16816(s1, qa[k][0][0], NR == 2 ? qa[k][NR - 1][0] : 0u, qa[k][0][1],
-                          NR == 2 ? qa[k][NR - 1][1] : 0u, hmul2(y[2 * e], sy[w / 2]),
-                          hmul2(y[2 * e + 1], sy[w / 2]));
+          for (int w = 0; w < D / 32; ++w) {
+            uint32_t x[4];
+            q4_unpack8(xw[w], x);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              qk(t, 2 * w + e, hmul2(x[2 * e], sx[w / 2]), hmul2(x[2 * e + 1], sx[w / 2]));
           }
         }
       }
       // ---- softmax weights
-      const bool half[2] = {(tag >> 30 & 1u) != 0, (tag >> 31) != 0};
-      const bool all_seen = tag >> 30 == 3u && t0 + 15 <= pos0 && (t0 >= lo_last || t0 + 15 < a.sink);
-      const int ta = t0 + 2 * c, tb = ta + 1, tc = ta + 8, td = ta + 9;
-      float x[NR][4];
+      // tokens of half 0 and 1: first + 0 .. HT - 1
+      const int ta = (int)tag.x, tb = (int)tag.y;
+      auto half_seen = [&](int t0) {
+        return t0 >= 0 && t0 + HT - 1 <= pos0 && (t0 >= lo_last || t0 + HT - 1 < a.sink);
+      };
+      const bool all_seen = half_seen(ta) && half_seen(tb);
+      auto token = [&](int t, int e) {  // of column 2c + e of tile t (negative: none)
+        const int first = 8 * t < HT ? ta : tb, off = 8 * t - (8 * t < HT ? 0 : HT) + 2 * c + e;
+        return first < 0 ? -1 : first + off;
+      };
+      if (!all_seen) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tt = token(t, e & 1), i = NR == 2 ? e >> 1 : 0;
+            if (!(tt >= 0 && tt <= pos[i] && (tt >= lo[i] || tt < a.sink))) s[t][e] = -INFINITY;
+          }
+      }
       bool grow = false;
+      float mx[NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        x[i][0] = s0[2 * i] * sl[i];
-        x[i][1] = s0[2 * i + 1] * sl[i];
-        x[i][2] = s1[2 * i] * sl[i];
-        x[i][3] = s1[2 * i + 1] * sl[i];
-        if (!all_seen) {
-          const int tt[4] = {ta, tb, tc, td};
+        mx[i] = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!(half[e >> 1] && tt[e] <= pos[i] && (tt[e] >= lo[i] || tt[e] < a.sink))) x[i][e] = -INFINITY;
-        }
-        grow |= fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) > m[i] + kSpSlack;
+        for (int t = 1; t < TT; ++t) mx[i] = fmaxf(mx[i], fmaxf(s[t][2 * i], s[t][2 * i + 1]));
+        grow |= mx[i] > thr[i];
       }
       if (__any_sync(0xffffffffu, grow)) {
         float f[NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          float mx = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[i], mx);
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+          const float mn = fmaxf(m[i], mx[i] * sl[i]);
           f[i] = mn == -INFINITY ? 1.f : ex2(m[i] - mn);
           m[i] = mn;
+          thr[i] = (mn + kSpSlack) / sl[i];
           l[i] *= f[i];
         }
 #pragma unroll
@@ -463,117 +578,135 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
           acc[t][3] *= f[NR - 1];
         }
       }
-      uint32_t pa[4];  // A operand of PV: rows n | n + 8, tokens 2c.. | + 8
+      // A operand of PV, k-step v: rows n | n + 8, tokens 16 v + 2c.. | + 8
+      uint32_t pa[TT / 2][4];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         const float base = m[i] == -INFINITY ? 0.f : m[i];
-        float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = ex2(x[i][e] - base);
-        l[i] += (p[0] + p[1]) + (p[2] + p[3]);
-        uint32_t h0, h1, e0, e1;
-        if constexpr (FMT == kSpanBf16) {
-          split_bf16x2(p[0], p[1], h0, e0);
-          split_bf16x2(p[2], p[3], h1, e1);
-        } else {
-          split_f16x2(p[0], p[1], h0, e0);
-          split_f16x2(p[2], p[3], h1, e1);
-        }
-        pa[i] = h0;
-        pa[2 + i] = h1;
-        if (NR == 1) {
-          pa[1] = e0;
-          pa[3] = e1;
+        for (int t = 0; t < TT; ++t) {
+          const float p0 = ex2(fmaf(s[t][2 * i], sl[i], -base));
+          const float p1 = ex2(fmaf(s[t][2 * i + 1], sl[i], -base));
+          l[i] += p0 + p1;
+          if constexpr (FMT == kSpanBf16) {
+            uint32_t hi, rest;
+            split_bf16x2(p0, p1, hi, rest);
+            pa[t / 2][2 * (t & 1) + i] = hi;
+            if (NR == 1) pa[t / 2][2 * (t & 1) + 1] = rest;
+          } else {
+            const __half2 hh = __floats2half2_rn(p0, p1);
+            pa[t / 2][2 * (t & 1) + i] = *reinterpret_cast<const uint32_t*>(&hh);
+            if (NR == 1) pa[t / 2][2 * (t & 1) + 1] = 0u;
+          }
         }
       }
-      // ---- latents: tokens 2c, 2c + 1 (+ 8) of the lane's columns
-      if constexpr (FMT == kSpanBf16) {
-        const int mi = lane >> 3, row = (lane & 7) + 8 * (mi & 1);
+      // ---- latents, 16 tokens a step.  Tokens that no row sees may hold
+      // anything (0 * NaN would poison the sums): they are taken as zeros.
 #pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-          const int ch = t + (mi >> 1);
-          const int sw = RV == 32 ? ch ^ ((row >> 1) & 3)
-                         : RV == 96 ? (ch < 8 ? ch ^ (row & 7) : 8 + ((ch ^ (row >> 1)) & 3))
-                                    : ch ^ (row & 7);
-          uint32_t b0, b1, b2, b3;
-          ldmatrix_x4_trans(zs + row * (2 * RV) + sw * 16, b0, b1, b2, b3);
-          mma_bf16_16816(acc[t], pa[0], pa[1], pa[2], pa[3], b0, b1);
-          mma_bf16_16816(acc[t + 1], pa[0], pa[1], pa[2], pa[3], b2, b3);
-        }
-      } else if constexpr (FMT == kSpanE4m3) {
-#pragma unroll
-        for (int w = 0; w < RV / 32; ++w) {
-          uint32_t v[4], f[2][4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = lds32(zs + (2 * c + (e & 1) + 8 * (e >> 1)) * RV + 32 * w + 4 * n);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // token pairs of each column
-            e4m3x4_to_f16(__byte_perm(v[2 * e], v[2 * e + 1], 0x5140), f[e][0], f[e][1]);
-            e4m3x4_to_f16(__byte_perm(v[2 * e], v[2 * e + 1], 0x7362), f[e][2], f[e][3]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16_16816(acc[4 * w + j], pa[0], pa[1], pa[2], pa[3], f[0][j], f[1][j]);
-        }
-      } else {
-        const uint32_t zsc = zs + 8 * RV;
-        const bool live[4] = {all_seen || seen(ta), all_seen || seen(tb), all_seen || seen(tc),
-                              all_seen || seen(td)};
-        // scale pairs of block k for tokens (2c, 2c + 1) and (+ 8); 0 for a
-        // token that no row sees, whose scale byte may be anything
-        auto scales = [&](int k, uint32_t& s01, uint32_t& s89) {
-          uint32_t v[4];
+      for (int v = 0; v < TT / 2; ++v) {
+        bool live[4] = {true, true, true, true};  // tokens 2c, 2c + 1, + 8, + 9 of the step
+        if (!all_seen) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            v[e] = lds8(zsc + (2 * c + (e & 1) + 8 * (e >> 1)) * (RV / 16) + k);
-            if (!live[e]) v[e] = 0;
+            const int tt = token(2 * v + (e >> 1), e & 1);
+            live[e] = tt >= 0 && tt <= p_last && (tt >= lo_first || tt < a.sink);
           }
-          s01 = (v[0] << 7) | (v[1] << 23);
-          s89 = (v[2] << 7) | (v[3] << 23);
-        };
-        auto pairs = [&](uint32_t x0, uint32_t y0, uint32_t (&f)[8]) {
-          uint32_t lo4[4], hi4[4];
-          q4_unpack8((x0 & 0x0f0f0f0fu) | ((y0 << 4) & 0xf0f0f0f0u), lo4);
-          q4_unpack8(((x0 >> 4) & 0x0f0f0f0fu) | (y0 & 0xf0f0f0f0u), hi4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[2 * j] = lo4[j];
-            f[2 * j + 1] = hi4[j];
-          }
-        };
-#pragma unroll
-        for (int w = 0; w < RV / 64; ++w) {
-          uint32_t v[4], f0[8], f1[8], s01, s89;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = lds32(zs + (2 * c + (e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * w + 4 * n);
-          pairs(v[0], v[1], f0);
-          pairs(v[2], v[3], f1);
-          scales(4 * w + (n >> 1), s01, s89);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            mma_f16_16816(acc[8 * w + j], pa[0], pa[1], pa[2], pa[3], hmul2(f0[j], s01),
-                          hmul2(f1[j], s89));
         }
-        if constexpr (RV % 64 != 0) {
-          constexpr int W0 = RV / 64;
-          uint32_t v[4], f0[8], f1[8], s01, s89;
+        if constexpr (FMT == kSpanQ4) {
+          const uint32_t zc = zs + (v ? zc1 : 0u) + 2 * c * (RV / 2);
+          const uint32_t zl = zs + (v ? zs1 : zs0) + 2 * c * (RV / 16);
+          // scale pairs of block k for tokens (2c, 2c + 1) and (+ 8, + 9)
+          auto scales = [&](int k, uint32_t& s01, uint32_t& s89) {
+            uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = lds16(zs + (2 * c + (e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * W0 + 2 * n);
-          pairs(v[0], v[1], f0);
-          pairs(v[2], v[3], f1);
-          scales(4 * W0 + (n >> 2), s01, s89);
+            for (int e = 0; e < 4; ++e) {
+              w[e] = lds8(zl + ((e & 1) + 8 * (e >> 1)) * (RV / 16) + k);
+              if (!all_seen && !live[e]) w[e] = 0;
+            }
+            s01 = __byte_perm(w[0], w[1], 0x5410) << 7;
+            s89 = __byte_perm(w[2], w[3], 0x5410) << 7;
+          };
+          auto pairs = [&](uint32_t x0, uint32_t y0, uint32_t (&f)[8]) {
+            uint32_t lo4[4], hi4[4];
+            q4_unpack8((x0 & 0x0f0f0f0fu) | ((y0 << 4) & 0xf0f0f0f0u), lo4);
+            q4_unpack8(((x0 >> 4) & 0x0f0f0f0fu) | (y0 & 0xf0f0f0f0u), hi4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16_16816(acc[8 * W0 + j], pa[0], pa[1], pa[2], pa[3], hmul2(f0[j], s01),
-                          hmul2(f1[j], s89));
+            for (int j = 0; j < 4; ++j) {
+              f[2 * j] = lo4[j];
+              f[2 * j + 1] = hi4[j];
+            }
+          };
+#pragma unroll
+          for (int w = 0; w < RV / 64; ++w) {
+            uint32_t x[4], f0[8], f1[8], s01, s89;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = lds32(zc + ((e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * w + 4 * n);
+            pairs(x[0], x[1], f0);
+            pairs(x[2], x[3], f1);
+            scales(4 * w + (n >> 1), s01, s89);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mma_f16_16816(acc[8 * w + j], pa[v][0], pa[v][1], pa[v][2], pa[v][3],
+                            hmul2(f0[j], s01), hmul2(f1[j], s89));
+          }
+          if constexpr (RV % 64 != 0) {
+            constexpr int W0 = RV / 64;
+            uint32_t x[4], f0[8], f1[8], s01, s89;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = lds16(zc + ((e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * W0 + 2 * n);
+            pairs(x[0], x[1], f0);
+            pairs(x[2], x[3], f1);
+            scales(4 * W0 + (n >> 2), s01, s89);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_f16_16816(acc[8 * W0 + j], pa[v][0], pa[v][1], pa[v][2], pa[v][3],
+                            hmul2(f0[j], s01), hmul2(f1[j], s89));
+          }
+        } else {
+          const uint32_t m0 = (live[0] ? 0xffffu : 0u) | (live[1] ? 0xffff0000u : 0u);
+          const uint32_t m1 = (live[2] ? 0xffffu : 0u) | (live[3] ? 0xffff0000u : 0u);
+          if constexpr (FMT == kSpanBf16) {
+            const int mi = lane >> 3, row = (lane & 7) + 8 * (mi & 1);
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+              uint32_t b0, b1, b2, b3;
+              ldmatrix_x4_trans(zs + row * (2 * RV) + sp_zchunk<RV>(row, t + (mi >> 1)) * 16, b0,
+                                b1, b2, b3);
+              if (!all_seen) b0 &= m0, b1 &= m1, b2 &= m0, b3 &= m1;
+              mma_bf16_16816(acc[t], pa[v][0], pa[v][1], pa[v][2], pa[v][3], b0, b1);
+              mma_bf16_16816(acc[t + 1], pa[v][0], pa[v][1], pa[v][2], pa[v][3], b2, b3);
+            }
+          } else {
+            const int F = a.zsplit;
+#pragma unroll
+            for (int w = 0; w < RV / 32; ++w) {
+              const int col = 32 * w + 4 * n;
+              const uint32_t at = zs + (col < F ? col : 16 * F + col - F);
+              const int pitch = col < F ? F : RV - F;
+              uint32_t x[4], f[2][4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = lds32(at + (2 * c + (e & 1) + 8 * (e >> 1)) * pitch);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {  // token pairs of each column
+                e4m3x4_to_f16(__byte_perm(x[2 * e], x[2 * e + 1], 0x5140), f[e][0], f[e][1]);
+                e4m3x4_to_f16(__byte_perm(x[2 * e], x[2 * e + 1], 0x7362), f[e][2], f[e][3]);
+              }
+              if (!all_seen) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[0][j] &= m0, f[1][j] &= m1;
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_f16_16816(acc[4 * w + j], pa[v][0], pa[v][1], pa[v][2], pa[v][3], f[0][j],
+                              f[1][j]);
+            }
+          }
         }
       }
     }
-    cp_async_wait_all();
-    __syncthreads();  // the rings become the meeting place
 
     // ---- the warps meet
 #pragma unroll
@@ -590,11 +723,10 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           row[2 + sp_col<FMT, RV>(t, 2 * c + e)] =
-              NR == 1 ? acc[t][e] + acc[t][2 + e] : acc[t][2 * i + e];
+              NR == 1 && FMT == kSpanBf16 ? acc[t][e] + acc[t][2 + e] : acc[t][2 * i + e];
     }
     __syncthreads();
-    const bool alone = u_begin == 0 && u_end == sq.n;  // the whole item is here
-    float* slot = a.partial + (size_t)(blockIdx.x + bg) * R * RS;
+    float* part = a.partial + (size_t)(blockIdx.x + bg) * R * RS;
     for (int o = tid; o < R * RV; o += kSpThreads) {
       const int r = o / RV, col = o - r * RV;
       float M = -INFINITY;
@@ -610,31 +742,31 @@ __global__ void __launch_bounds__(kSpThreads, FMT == kSpanBf16 || NR == 2 ? 1 : 
       }
       if (alone) {
         const int j = r / a.G, h = r - j * a.G;
-        a.out[(((size_t)b * a.n_tot + a.j0 + j) * a.Hq + g * a.G + h) * RV + col] =
+        a.out[(((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV + col] =
             f_to_bf16(L > 0.f ? A / L : 0.f);
       } else {
-        slot[r * RS + 2 + col] = A;
+        part[r * RS + 2 + col] = A;
         if (col == 0) {
-          slot[r * RS] = M;
-          slot[r * RS + 1] = L;
+          part[r * RS] = M;
+          part[r * RS + 1] = L;
         }
       }
     }
-    __syncthreads();  // the meeting place becomes rings again
-    seg = x0 + u_end;
+    __syncthreads();  // the meeting place is free again
+    seg = item_end;
   }
 }
 
 // Joins the partials of the items that several CTAs share; rows of items
-// without units are zero.  One CTA per (sequence, KV head).
-template <int RV>
+// without units are zero.  One CTA per (sequence, KV head).  The lengths are
+// read before the grid-dependency wait: the launch before this one let it in
+// after its own wait, and does not write them.
+template <int UT, int RV>
 __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int grid) {
   constexpr int RS = RV + 2;
   __shared__ long long pre[257];
-  pdl_wait();
-  pdl_launch_dependents();
-  span_scan(a, pre, false);
-  const int bg = blockIdx.x, b = bg / a.Hkv, g = bg - b * a.Hkv, R = a.n_q * a.G;
+  span_scan<UT>(a, pre, false);
+  const int bg = blockIdx.x, b = bg / a.Hkv, g = bg - b * a.Hkv, R = a.n_tot * a.G;
   const long long total = pre[a.B] * a.Hkv, u = pre[b + 1] - pre[b];
   const long long x0 = pre[b] * a.Hkv + g * u;
   int c0 = 0, c1 = -1;
@@ -642,8 +774,10 @@ __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int 
     const int C = span_ctas(total, grid);
     c0 = span_cta_of(x0, total, C);
     c1 = span_cta_of(x0 + u - 1, total, C);
-    if (c0 == c1) return;  // written by its one CTA
   }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (u > 0 && c0 == c1) return;  // written by its one CTA
   for (int o = threadIdx.x; o < R * RV; o += kSpThreads) {
     const int r = o / RV, col = o - r * RV;
     float M = -INFINITY, L = 0.f, A = 0.f;
@@ -659,40 +793,39 @@ __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int 
       M = mn;
     }
     const int j = r / a.G, h = r - j * a.G;
-    a.out[(((size_t)b * a.n_tot + a.j0 + j) * a.Hq + g * a.G + h) * RV + col] =
+    a.out[(((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV + col] =
         f_to_bf16(L > 0.f ? A / L : 0.f);
   }
 }
 
 template <int FMT, int D, int RV, int NR>
 cudaError_t launch_span_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
+  constexpr int UT = sp_unit<FMT>();
   // Units of the longest context this call may meet; fewer CTAs when they do
   // not suffice for kSpMinUnits each.
-  const long long span = a.sel ? (long long)a.top_k * a.S
-                         : a.window > 0 ? (long long)a.window + a.n_q + a.sink + 48
-                                        : (long long)a.max_seq_len + 16;
-  const long long most = span < (long long)a.max_seq_len + 16 || a.sel
-                             ? span : (long long)a.max_seq_len + 16;
-  const long long units = (most + 15) / 16 * a.B * a.Hkv;
-  long long grid = (long long)num_sms() * (FMT == kSpanBf16 || NR == 2 ? 1 : 2);
+  long long most = (long long)a.max_seq_len + UT;
+  if (a.sel)
+    most = (long long)a.top_k * a.S;
+  else if (a.window > 0 && (long long)a.window + a.n_tot + a.sink + 3 * UT < most)
+    most = (long long)a.window + a.n_tot + a.sink + 3 * UT;
+  const long long units = (most + UT - 1) / UT * a.B * a.Hkv;
+  long long grid = (long long)num_sms() * sp_ctas<FMT, NR>();
   if (grid > kSpanMaxCtas) grid = kSpanMaxCtas;
   if (grid > units / kSpMinUnits) grid = units / kSpMinUnits > 0 ? units / kSpMinUnits : 1;
   constexpr size_t smem = sp_smem<FMT, D, RV, NR>();
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(span_kernel<FMT, D, RV, NR>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t e = launch_k(span_kernel<FMT, D, RV, NR>, dim3((unsigned)grid), dim3(kSpThreads),
-                           smem, st, pdl, a);
+  cudaError_t e = cudaFuncSetAttribute(span_kernel<FMT, D, RV, NR>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_k(span_merge_kernel<RV>, dim3(a.B * a.Hkv), dim3(kSpThreads), 0, st, pdl, a,
+  e = launch_k(span_kernel<FMT, D, RV, NR>, dim3((unsigned)grid), dim3(kSpThreads), smem, st, pdl,
+               a);
+  if (e != cudaSuccess) return e;
+  return launch_k(span_merge_kernel<UT, RV>, dim3(a.B * a.Hkv), dim3(kSpThreads), 0, st, pdl, a,
                   (int)grid);
 }
 
 template <int FMT>
 cudaError_t launch_span_fmt(const SpanArgs& a, cudaStream_t st, bool pdl) {
-  const bool two = a.n_q * a.G > 8;
+  const bool two = a.n_tot * a.G > 8;
 #define BKV_SPAN_RV(DD)                                                       \
   switch (a.r_v) {                                                            \
     case 32:                                                                  \
