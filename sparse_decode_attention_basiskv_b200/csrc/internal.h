@@ -291,6 +291,7 @@ inline size_t span_slots(int B, int Hkv) { return (size_t)kSpanMaxCtas + (size_t
 cudaError_t launch_span_bf16(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_e4m3(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_q4(const SpanArgs& a, cudaStream_t st, bool pdl);
+cudaError_t launch_span_q4_p32(const SpanArgs& a, cudaStream_t st, bool pdl);
 
 // Prompt form (tensor cores; no selection): work items
 // of two row tiles, each cut into nsplit runs of KV tiles while the items

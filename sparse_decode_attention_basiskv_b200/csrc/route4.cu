@@ -5,18 +5,19 @@
 //
 // with the folded queries in fp32 (fold_query_kernel).  One pass over the z
 // and e pages: (r_v + r_k) * 9 / 16 bytes a token and KV head, so HBM bounds
-// it, closely followed by the instructions that widen the codes (one
-// conversion and one multiplication for two columns).
+// it, closely followed by the instructions that widen the codes (a conversion
+// and a multiplication for two columns).
 //
-// The pages of all (sequence, KV head) items form one line, cut into equal
-// contiguous runs, one a warp (a scan of the lengths finds them, so ragged
-// batches load every SM alike).  A warp copies its 16-token units (cp.async)
-// into its own ring kStages - 1 units ahead.  Tokens are the columns of
-// mma.m16n8k16's B operand, as stored; the rows of A are the group's heads:
-// rows 0-7 hold the f16 roundings of the folded queries, rows 8-15 their
-// remainders, so one product gives fp32-accurate scores (22 significant
-// bits; each head is first scaled by a power of two that puts its largest
-// magnitude into [2^14, 2^15), divided out of the scores again).
+// The units (32 tokens: one page of 32 or two of 16) of all (sequence, KV
+// head) items form one line, cut into equal contiguous runs, one a warp (a
+// scan of the lengths finds them, so ragged batches load every SM alike).  A
+// warp brings its units into its own ring, kR4Stages - 1 ahead: a tile is one
+// contiguous piece that one lane hands to the copy engine.  Tokens are the
+// rows of mma.m16n8k16's A operand, as stored; B holds four heads, the f16
+// roundings of their folded queries in the even columns and the remainders in
+// the odd ones, so a lane's two sums give one fp32-accurate score (22
+// significant bits; each head is first scaled by a power of two that puts its
+// largest magnitude into [2^14, 2^15), divided out of the scores again).
 #include "cache4.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -28,85 +29,198 @@ namespace {
 
 constexpr int kR4Threads = kLineMaxSeqs;  // a thread scans a sequence's length
 constexpr int kR4Warps = kR4Threads / 32;
-constexpr int kR4Stages = 4;
+constexpr int kR4Unit = 32;
 constexpr int kR4CtasPerSm = 2;
 
-// Adds the products of one part (W columns at `codes`, its scales behind
-// them) to the scores of tokens n (s0) and n + 8 (s1).  Lane c holds columns
-// W / 4 * c .., 4 of them a k-step.
-template <int W, int K0, int KS>
-__device__ __forceinline__ void r4_part(uint32_t codes, int n, int c, const uint32_t (&qh)[KS][2],
-                                        const uint32_t (&ql)[KS][2], float (&s0)[4],
-                                        float (&s1)[4]) {
-  const uint32_t sc = codes + 8 * W;
+// Ring depth: 4 units, 3 where shared memory ends.
+template <int W>
+constexpr int r4_stages() {
+  return 4 * kR4Warps * 18 * W <= 104 * 1024 ? 4 : 3;
+}
+
+// The warp's maximum.
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Adds the products of one part (W columns, 16 tokens whose codes start at
+// `codes` and scales at `sc`) to the scores of tokens n and n + 8.  Lane c
+// holds columns W / 4 * c .., 4 of them a k-step.
+template <int W, int K0, int KS, int NJ>
+__device__ __forceinline__ void r4_part(uint32_t codes, uint32_t sc, int n, int c,
+                                        const uint32_t (&qb)[KS][NJ][2], float (&s)[NJ][4]) {
+  auto step = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) mma_f16_16816(s[j], a0, a1, a2, a3, qb[k][j][0], qb[k][j][1]);
+  };
+  const uint32_t row = codes + n * (W / 2) + (W / 8) * c;
   if constexpr (W == 16) {
     // the lane's half of a 32-bit word
     uint32_t x[4], y[4];
+    const uint32_t at = codes + n * 8 + 4 * (c >> 1);
     const int sh = 16 * (c & 1);
-    q4_unpack8(lds32(codes + n * 8 + 4 * (c >> 1)) >> sh, x);
-    q4_unpack8(lds32(codes + (n + 8) * 8 + 4 * (c >> 1)) >> sh, y);
+    q4_unpack8(lds32(at) >> sh, x);
+    q4_unpack8(lds32(at + 64) >> sh, y);
     const uint32_t sx = q4_scale_x2(lds8(sc + n)), sy = q4_scale_x2(lds8(sc + n + 8));
-    mma_f16_16816(s0, qh[K0][0], ql[K0][0], qh[K0][1], ql[K0][1], hmul2(x[0], sx), hmul2(x[1], sx));
-    mma_f16_16816(s1, qh[K0][0], ql[K0][0], qh[K0][1], ql[K0][1], hmul2(y[0], sy), hmul2(y[1], sy));
+    step(K0, hmul2(x[0], sx), hmul2(y[0], sy), hmul2(x[1], sx), hmul2(y[1], sy));
   } else {
-    uint32_t sx = 0, sy = 0;
+    uint32_t xw[W / 32], yw[W / 32], sx = 0, sy = 0;
+    if constexpr (W == 128) {
+      const uint4 x = lds128(row), y = lds128(row + 8 * (W / 2));
+      xw[0] = x.x, xw[1] = x.y, xw[2] = x.z, xw[3] = x.w;
+      yw[0] = y.x, yw[1] = y.y, yw[2] = y.z, yw[3] = y.w;
+    } else if constexpr (W == 64) {
+      const uint2 x = lds64(row), y = lds64(row + 8 * (W / 2));
+      xw[0] = x.x, xw[1] = x.y;
+      yw[0] = y.x, yw[1] = y.y;
+    } else {
+#pragma unroll
+      for (int w = 0; w < W / 32; ++w) {
+        xw[w] = lds32(row + 4 * w);
+        yw[w] = lds32(row + 8 * (W / 2) + 4 * w);
+      }
+    }
 #pragma unroll
     for (int w = 0; w < W / 32; ++w) {  // 8 columns
       uint32_t x[4], y[4];
-      q4_unpack8(lds32(codes + n * (W / 2) + (W / 8) * c + 4 * w), x);
-      q4_unpack8(lds32(codes + (n + 8) * (W / 2) + (W / 8) * c + 4 * w), y);
+      q4_unpack8(xw[w], x);
+      q4_unpack8(yw[w], y);
       if (W % 64 != 0 || w % 2 == 0) {
         const int blk = ((W / 4) * c + 8 * w) >> 4;
         sx = q4_scale_x2(lds8(sc + n * (W / 16) + blk));
         sy = q4_scale_x2(lds8(sc + (n + 8) * (W / 16) + blk));
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = K0 + 2 * w + e;
-        mma_f16_16816(s0, qh[k][0], ql[k][0], qh[k][1], ql[k][1], hmul2(x[2 * e], sx),
-                      hmul2(x[2 * e + 1], sx));
-        mma_f16_16816(s1, qh[k][0], ql[k][0], qh[k][1], ql[k][1], hmul2(y[2 * e], sy),
-                      hmul2(y[2 * e + 1], sy));
-      }
+      for (int e = 0; e < 2; ++e)
+        step(K0 + 2 * w + e, hmul2(x[2 * e], sx), hmul2(y[2 * e], sy), hmul2(x[2 * e + 1], sx),
+             hmul2(y[2 * e + 1], sy));
     }
   }
 }
 
-template <int RV, int RK>
+// NJ: groups of four heads (1 for G <= 4, 2 for G = 8).  ONE: pages of 32.
+template <int RV, int RK, int NJ, bool ONE>
 __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4Args a) {
-  constexpr int W = RV + RK, KS = W / 16, UB = 9 * W, NST = kR4Stages;
-  extern __shared__ __align__(16) uint8_t r4_smem[];
+  constexpr int W = RV + RK, KS = W / 16, UB = 18 * W, NST = r4_stages<W>();
+  constexpr int PP = ONE ? 1 : 2;  // pages a unit
+  extern __shared__ __align__(128) uint8_t r4_smem[];
   __shared__ long long pre[257];
+  __shared__ uint64_t bars[kR4Warps * NST];
+  __shared__ uint2 tags[kR4Warps][NST];  // the unit's pages: 1 there, 0 missing
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(r4_smem) + warp * NST * UB;
-  const int logS = 31 - __clz(a.S), upp = a.S >> 4;  // units a page: 1 or 2
+  const uint32_t bar = smem_u32(bars + warp * NST);
 
+  if (tid < kR4Warps * NST) mbar_init(bars + tid, 1);
+  fence_barrier_init();
   pdl_wait();
   pdl_launch_dependents();
-  line_scan(a.B, pre, [&](int b) -> long long {  // pages
+  auto units_of = [&](int len) {
+    return len >= 0 && len <= a.max_seq_len ? (len + kR4Unit - 1) / kR4Unit : 0;
+  };
+  line_scan(a.B, pre, [&](int b) -> long long {
     const int len = a.seq_lens[b];
-    if (len >= 0 && len <= a.max_seq_len) return (len + a.S - 1) >> logS;
-    if (blockIdx.x == 0) raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
-    return 0;
+    if (blockIdx.x == 0 && (len < 0 || len > a.max_seq_len))
+      raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
+    return units_of(len);
   });
   const long long total = pre[a.B] * a.Hkv;
-  const long long W_all = (long long)gridDim.x * kR4Warps;
+  const long long n_warps = (long long)gridDim.x * kR4Warps;
   const long long w_id = (long long)blockIdx.x * kR4Warps + warp;
-  const long long end = total * (w_id + 1) / W_all;
-  long long seg = total * w_id / W_all;
-  int b = seg < end ? line_find(a.B, pre, a.Hkv, seg) : 0;
-  while (seg < end) {
-    while (pre[b + 1] * a.Hkv <= seg) ++b;
-    const int P = (int)(pre[b + 1] - pre[b]);
-    const int g = (int)((seg - pre[b] * a.Hkv) / P);
-    const long long x0 = pre[b] * a.Hkv + (long long)g * P;
-    const int p0 = (int)(seg - x0), p1 = (int)min((long long)P, end - x0);
-    const int T = a.seq_lens[b];
-    // ---- folded queries of head n: f16 hi and lo
-    uint32_t qh[KS][2], ql[KS][2];
-    float inv;
+  const long long start = total * w_id / n_warps;
+  const int run = (int)(total * (w_id + 1) / n_warps - start);
+
+  // Physical pages of 32 units ahead, one a lane (-1: not there).
+  int id_a = -1, id_b = -1, id_g = 0, id_base = 0;
+  auto fetch_ids = [&](int base) {
+    id_base = base;
+    id_a = id_b = -1;
+    if (base + lane >= run) return;
+    const long long x = start + base + lane;
+    const int b = line_find(a.B, pre, a.Hkv, x);
+    const int U = (int)(pre[b + 1] - pre[b]);
+    const long long y = x - pre[b] * a.Hkv;
+    id_g = (int)(y / U);
+    const int p = (int)(y - (long long)id_g * U) * PP;
+    const int P = (a.seq_lens[b] + a.S - 1) / a.S;
+    auto look = [&](int q) {
+      int id = q < P ? __ldg(a.block_table + (size_t)b * a.max_pages + q) : -1;
+      if (q < P && (id < 0 || id >= a.num_phys)) {
+        raise_status(a.status, BASISKV_DEV_BAD_PAGE);
+        id = -1;
+      }
+      return id;
+    };
+    id_a = look(p);
+    if (PP == 2) id_b = look(p + 1);
+  };
+  auto issue = [&](int k, int slot) {
+    if (k >= run) return;
+    if (k - id_base >= 32) fetch_ids(k);
+    if (lane != k - id_base) return;
+    const uint32_t st = ring + slot * UB, b = bar + 8 * slot;
+    auto copy = [&](uint32_t dst, const uint8_t* src, uint32_t bytes) {
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+          "[%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(b)
+          : "memory");
+    };
+    const int present = (id_a >= 0) + (id_b >= 0);
+    tags[warp][slot] = make_uint2(id_a >= 0, id_b >= 0);
+    if (!present) {
+      asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(b)
+                   : "memory");
+      return;
+    }
+    constexpr int TZ = (ONE ? 18 : 9) * RV, TE = (ONE ? 18 : 9) * RK;  // tile bytes
+    asm volatile(
+        "{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(b),
+        "r"(present * (TZ + TE))
+        : "memory");
+    if (id_a >= 0) {
+      const size_t t = (size_t)id_a * a.Hkv + id_g;
+      copy(st, a.Z + t * TZ, TZ);
+      copy(st + 18 * RV, a.E + t * TE, TE);
+    }
+    if (id_b >= 0) {
+      const size_t t = (size_t)id_b * a.Hkv + id_g;
+      copy(st + 9 * RV, a.Z + t * TZ, TZ);
+      copy(st + 18 * RV + 9 * RK, a.E + t * TE, TE);
+    }
+  };
+  int k_next = 0, slot_next = 0;
+  auto request = [&]() {
+    issue(k_next++, slot_next);
+    slot_next = slot_next + 1 == NST ? 0 : slot_next + 1;
+  };
+  if (run > 0) fetch_ids(0);
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) request();
+  int slot = 0;
+  uint32_t phase = 0;
+
+  for (int seg = 0; seg < run;) {
+    int b, g, u0, item_end;
     {
-      const float* qr = a.qt + ((size_t)b * a.Hq + g * a.G + (n < a.G ? n : 0)) * W;
+      const long long x = start + seg;
+      b = line_find(a.B, pre, a.Hkv, x);
+      const int U = (int)(pre[b + 1] - pre[b]);
+      const long long y = x - pre[b] * a.Hkv;
+      g = (int)(y / U);
+      u0 = (int)(y - (long long)g * U);
+      item_end = min(run, seg + U - u0);
+    }
+    const int T = a.seq_lens[b];
+    float* out = a.scores + ((size_t)b * a.Hkv + g) * a.max_pages;
+    // ---- folded queries: column n of group j is head 4 j + n / 2, part n % 2
+    uint32_t qb[KS][NJ][2];
+    float inv[NJ];  // of head 4 j + c, whose scores the lane gets
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int h = 4 * j + (n >> 1);
+      const float* qr = a.qt + ((size_t)b * a.Hq + g * a.G + (h < a.G ? h : 0)) * W;
       float f[KS][4], m = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -115,7 +229,7 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
         f[k][0] = v.x, f[k][1] = v.y, f[k][2] = v.z, f[k][3] = v.w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (n >= a.G) f[k][e] = 0.f;
+          if (h >= a.G) f[k][e] = 0.f;
           m = fmaxf(m, fabsf(f[k][e]));
         }
       }
@@ -124,122 +238,92 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
       const int ex = m > 0.f ? (int)((__float_as_uint(m) >> 23) & 0xffu) - 126 : 15;
       const int sh = max(-126, min(126, 15 - ex));
       const float sc = __uint_as_float((uint32_t)(127 + sh) << 23);
-      inv = __uint_as_float((uint32_t)(127 - sh) << 23);
+      const int shc = __shfl_sync(0xffffffffu, sh, 8 * c);
+      inv[j] = __uint_as_float((uint32_t)(127 - shc) << 23);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          split_f16x2(f[k][2 * e] * sc, f[k][2 * e + 1] * sc, qh[k][e], ql[k][e]);
-    }
-    // ---- pages p0 .. p1 - 1, unit u = page * upp + half
-    const int count = (p1 - p0) * upp;
-    int id = -1, id_base = 0;  // physical pages of 32 pages, one a lane
-    auto fetch_ids = [&](int base) {
-      id_base = base;
-      id = -1;
-      if (p0 + base + lane < p1) {
-        id = __ldg(a.block_table + (size_t)b * a.max_pages + p0 + base + lane);
-        if (id < 0 || id >= a.num_phys) {
-          raise_status(a.status, BASISKV_DEV_BAD_PAGE);
-          id = -1;
+        for (int e = 0; e < 2; ++e) {
+          uint32_t hi, lo;
+          split_f16x2(f[k][2 * e] * sc, f[k][2 * e + 1] * sc, hi, lo);
+          qb[k][j][e] = n & 1 ? lo : hi;
         }
+    }
+    for (; seg < item_end; ++seg, ++u0) {
+      __syncwarp();
+      request();
+      mbar_wait(bars + warp * NST + slot, phase, a.status);
+      const uint2 tag = tags[warp][slot];
+      const uint32_t st = ring + slot * UB;
+      if (++slot == NST) {
+        slot = 0;
+        phase ^= 1;
       }
-    };
-    auto issue = [&](int u) {
-      if (u < count) {
-        const int p = u >> (upp - 1);
-        if (p - id_base >= 32) fetch_ids(p);
-        const int pp = __shfl_sync(0xffffffffu, id, p - id_base);
-        if (pp >= 0) {
-          const int row = upp == 2 && (u & 1) ? 16 : 0;
-          const size_t tile = (size_t)pp * a.Hkv + g;
-          const uint8_t* zt = a.Z + tile * q4_tile_bytes(a.S, RV);
-          const uint8_t* et = a.E + tile * q4_tile_bytes(a.S, RK);
-          const uint32_t st = ring + (u % NST) * UB;
+      const int t0 = u0 * kR4Unit;
+      float best[2];
 #pragma unroll
-          for (int x = 0; x < 9 * W / 16; x += 32) {
-            const int i = x + lane;
-            const uint8_t* src;
-            if (i < RV / 2)
-              src = zt + row * (RV / 2) + 16 * i;
-            else if (i < RV / 16 * 9)
-              src = zt + a.S * (RV / 2) + row * (RV / 16) + 16 * (i - RV / 2);
-            else if (i < RV / 16 * 9 + RK / 2)
-              src = et + row * (RK / 2) + 16 * (i - RV / 16 * 9);
-            else
-              src = et + a.S * (RK / 2) + row * (RK / 16) + 16 * (i - RV / 16 * 9 - RK / 2);
-            if (i < 9 * W / 16) cp_async16_or_zero(st + 16 * i, src);
+      for (int v = 0; v < 2; ++v) {
+        float s[NJ][4];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        constexpr int H1 = ONE ? 8 : 9, S0 = ONE ? 16 : 8, S1 = 17;
+        r4_part<RV, 0, KS, NJ>(st + v * H1 * RV, st + (v ? S1 : S0) * RV, n, c, qb, s);
+        r4_part<RK, RV / 16, KS, NJ>(st + 18 * RV + v * H1 * RK,
+                                     st + 18 * RV + (v ? S1 : S0) * RK, n, c, qb, s);
+        float x = -INFINITY, y = -INFINITY;  // tokens n and n + 8
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          if (4 * j + c < a.G) {
+            x = fmaxf(x, (s[j][0] + s[j][1]) * inv[j]);
+            y = fmaxf(y, (s[j][2] + s[j][3]) * inv[j]);
           }
+        if (t0 + kR4Unit > T) {  // the last unit's tail
+          if (t0 + 16 * v + n >= T) x = -INFINITY;
+          if (t0 + 16 * v + n + 8 >= T) y = -INFINITY;
         }
+        best[v] = fmaxf(x, y);
       }
-      cp_async_commit();
-    };
-    fetch_ids(0);
-    // a page's physical id is looked up again when it is scored
-    int sid = id, sid_base = 0;
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i) issue(i);
-    float best = -INFINITY;
-    for (int u = 0; u < count; ++u) {
-      __syncwarp();
-      issue(u + NST - 1);
-      cp_async_wait_group<NST - 1>();
-      __syncwarp();
-      const int p = u >> (upp - 1);
-      if (p - sid_base >= 32) {
-        sid_base = p;
-        sid = -1;
-        if (p0 + p + lane < p1) {
-          sid = __ldg(a.block_table + (size_t)b * a.max_pages + p0 + p + lane);
-          if (sid >= a.num_phys) sid = -1;
-        }
-      }
-      const bool there = __shfl_sync(0xffffffffu, sid, p - sid_base) >= 0;
-      const uint32_t st = ring + (u % NST) * UB;
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-      r4_part<RV, 0, KS>(st, n, c, qh, ql, s0, s1);
-      r4_part<RK, RV / 16, KS>(st + 9 * RV, n, c, qh, ql, s0, s1);
-      const int t0 = ((p0 + p) << logS) + 16 * (u & (upp - 1));
-      float v[4] = {s0[0] + s0[2], s0[1] + s0[3], s1[0] + s1[2], s1[1] + s1[3]};
-      if (t0 + 16 > T) {  // the last page's tail
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (t0 + 2 * c + (e & 1) + 8 * (e >> 1) >= T) v[e] = -INFINITY;
-      }
-      if (there && n < a.G)
-        best = fmaxf(best, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * inv);
-      if ((u & (upp - 1)) == upp - 1) {
-        best = warp_max(best);
-        if (lane == 0) a.scores[((size_t)b * a.Hkv + g) * a.max_pages + p0 + p] = best;
-        best = -INFINITY;
+      if (ONE) {
+        const float r = redux_max(fmaxf(best[0], best[1]));
+        if (lane == 0) out[u0] = tag.x ? r : -INFINITY;
+      } else {
+        const float r0 = redux_max(best[0]), r1 = redux_max(best[1]);
+        // the second page exists when the unit's first token past it does
+        if (lane < 2 && (lane == 0 || t0 + 16 < T))
+          out[2 * u0 + lane] = (lane ? tag.y : tag.x) ? (lane ? r1 : r0) : -INFINITY;
       }
     }
-    cp_async_wait_all();
-    __syncwarp();
-    seg = x0 + p1;
   }
 }
 
-template <int RV, int RK>
+template <int RV, int RK, int NJ, bool ONE>
 cudaError_t launch_route4_t(const Route4Args& a, cudaStream_t st, bool pdl) {
-  constexpr size_t smem = (size_t)kR4Warps * kR4Stages * 9 * (RV + RK);
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(route4_kernel<RV, RK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  const long long pages = (long long)((a.max_seq_len + a.S - 1) / a.S) * a.B * a.Hkv;
+  constexpr size_t smem = (size_t)kR4Warps * r4_stages<RV + RK>() * 18 * (RV + RK);
+  cudaError_t e = cudaFuncSetAttribute(route4_kernel<RV, RK, NJ, ONE>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)((a.max_seq_len + kR4Unit - 1) / kR4Unit) * a.B * a.Hkv;
   long long grid = (long long)num_sms() * kR4CtasPerSm;
-  if (grid > pages / kR4Warps) grid = pages / kR4Warps > 0 ? pages / kR4Warps : 1;
-  return launch_k(route4_kernel<RV, RK>, dim3((unsigned)grid), dim3(kR4Threads), smem, st, pdl, a);
+  if (grid > units / kR4Warps) grid = units / kR4Warps > 0 ? units / kR4Warps : 1;
+  return launch_k(route4_kernel<RV, RK, NJ, ONE>, dim3((unsigned)grid), dim3(kR4Threads), smem,
+                  st, pdl, a);
+}
+
+template <int RV, int RK>
+cudaError_t launch_route4_p(const Route4Args& a, cudaStream_t st, bool pdl) {
+  if (a.S == 32)
+    return a.G == 8 ? launch_route4_t<RV, RK, 2, true>(a, st, pdl)
+                    : launch_route4_t<RV, RK, 1, true>(a, st, pdl);
+  return a.G == 8 ? launch_route4_t<RV, RK, 2, false>(a, st, pdl)
+                  : launch_route4_t<RV, RK, 1, false>(a, st, pdl);
 }
 
 template <int RV>
 cudaError_t launch_route4_rk(const Route4Args& a, cudaStream_t st, bool pdl) {
   switch (a.r_k) {
-    case 16: return launch_route4_t<RV, 16>(a, st, pdl);
-    case 32: return launch_route4_t<RV, 32>(a, st, pdl);
-    default: return launch_route4_t<RV, 64>(a, st, pdl);
+    case 16: return launch_route4_p<RV, 16>(a, st, pdl);
+    case 32: return launch_route4_p<RV, 32>(a, st, pdl);
+    default: return launch_route4_p<RV, 64>(a, st, pdl);
   }
 }
 

@@ -5,8 +5,9 @@
 //   a[row] = sum_t p_t z_t,  p = softmax over the row's tokens of
 //   (q . K_t) / sqrt(d)
 //
-// Rows: query token j and head h of KV head g make row j * G + h; up to 16
-// rows (the M of mma.m16n8k16) share every Key and latent that is read.
+// Rows: query token j and head h of KV head g make row j * G + h; 8 or 16 rows
+// (one or two N tiles of mma.m16n8k16) share every Key and latent that is
+// read.
 // Bound by HBM: 2 (d + r_v) multiply-adds a row and (d + r_v) cached columns
 // a token; over 4-bit caches closely followed by the instructions that widen
 // the codes (a conversion and a multiplication for two columns).
@@ -27,10 +28,11 @@
 // hands them to the copy engine (cp.async.bulk), which costs a few
 // instructions a unit where 16-byte copies by all lanes cost 40 (a gather of
 // 1152 + 576 byte tiles alone runs at 6.2 TB/s this way).  bf16 units are
-// copied 16 bytes a lane, swizzled for ldmatrix.  The Keys are the B operand
-// of QK (columns = tokens, as stored), so the scores arrive with a row's
-// tokens in the layout of the A operand of PV and need no transposition; the
-// latents are PV's B operand.
+// copied 16 bytes a lane, swizzled for ldmatrix.  The Keys are the A operand
+// of QK (rows = tokens, the head dimension in the order the lanes hold it) and
+// the latents PV's A operand (rows = latent columns: a lane reads the same
+// columns of neighbouring tokens and pairs them); the scores, [token][row],
+// become PV's B operand with one 8x8 transposition per 8 tokens.
 //
 // The running maximum moves only when a score passes it by 8 (a factor of
 // 256 in the weights, far inside the range of f16): then the warp takes the
@@ -39,8 +41,7 @@
 // Precision: scores and sums in fp32.  The weights of PV are rounded to f16
 // (2^-12 of each weight, an eighth of the output's own rounding) where the
 // operands are f16, and held as bf16 roundings plus bf16 remainders (16
-// significant bits, the remainders in the rows of A that at most 8 query rows
-// leave free) or, with more than 8 rows, as bf16 where they are bf16.
+// significant bits, a second product) where they are bf16.
 //
 // Formats: bf16 (bf16 products), E4M3 and 4 bits (widened to f16, which is
 // exact; each row's query is brought to f16 by a power of two that puts its
@@ -163,11 +164,12 @@ __device__ __forceinline__ void mbar_arrive_only(uint32_t bar) {
                : "memory");
 }
 
-template <int FMT, int D, int RV, int NR>
+// ONE (4-bit caches): a unit is one page of 32 tokens, else two of 16.
+template <int FMT, int D, int RV, int NR, bool ONE>
 __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(SpanArgs a) {
   constexpr int UT = sp_unit<FMT>(), HT = UT / 2;  // tokens of a unit, of its halves
-  constexpr int TT = UT / 8;                       // 8-token column tiles of QK
-  constexpr int NT = RV / 8, KS = D / 16, NST = sp_stages<FMT, D, RV, NR>();
+  constexpr int VT = UT / 16;                      // 16-token steps
+  constexpr int MT = RV / 16, KS = D / 16, NST = sp_stages<FMT, D, RV, NR>();
   constexpr int UB = sp_unit_bytes<FMT, D, RV>();
   constexpr int RS = RV + 2;
   constexpr bool BULK = FMT != kSpanBf16;
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
         id_tb = selected(2 * u + 1);
       }
       if (id_ta >= 0) id_ra = tile_row(id_ta);
-      if (a.S >= UT ? id_ta >= 0 : id_tb >= 0) id_rb = tile_row(id_tb);
+      if ((FMT == kSpanQ4 ? ONE : a.S >= UT) ? id_ta >= 0 : id_tb >= 0) id_rb = tile_row(id_tb);
     } else {
       id_ta = UT * (u < sq.n_sink ? u : sq.lo_unit + u - sq.n_sink);
       id_tb = id_ta + HT;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
           if (!present) {
             mbar_arrive_only(b);
           } else if constexpr (FMT == kSpanQ4) {
-            if (a.S >= UT) {  // the unit is one tile: codes and scales of 32 rows
+            if constexpr (ONE) {  // the unit is one tile: codes and scales of 32 rows
               const size_t tile = (id_ra >= 0 ? id_ra : id_rb - HT) >> a.logS;
               expect(UB);
               copy(st, a.K + tile * (2 * 9 * D), 2 * 9 * D);
@@ -357,13 +359,11 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
   int slot = 0;
   uint32_t phase = 0;  // of the slots' barriers in this turn of the ring
 
-  // Byte offsets within a unit that depend on the page size (4 bits only): the
-  // second half's codes and the scales.
-  const bool one_tile = a.S >= UT;
-  const uint32_t kc1 = one_tile ? 8 * D : 9 * D, ks0 = one_tile ? 16 * D : 8 * D,
-                 ks1 = one_tile ? 17 * D : 17 * D;
-  const uint32_t zc1 = one_tile ? 8 * RV : 9 * RV, zs0 = one_tile ? 16 * RV : 8 * RV,
-                 zs1 = one_tile ? 17 * RV : 17 * RV;
+  // 4-bit units: byte offsets of half 1's codes and of the halves' scales
+  // (Keys; the latents' are the same with RV for D), and of the lane in them
+  constexpr int H1 = ONE ? 8 : 9, S0 = ONE ? 16 : 8, S1 = 17;
+  const uint32_t lane_k = n * (D / 2) + (D / 8) * c, lane_ks = n * (D / 16) + (D / 64) * c;
+  const uint32_t lane_z = 2 * c * (RV / 2) + 4 * n, lane_zs = 2 * c * (RV / 16) + (n >> 1);
 
   int seg = 0;  // the run's next unit
   while (seg < run) {
@@ -388,26 +388,30 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
     const int lo_first = a.window > 0 ? max(0, max(pos0, 0) - a.window + 1) : 0;
     const int lo_last = a.window > 0 ? max(0, p_last - a.window + 1) : 0;
 
-    // ---- queries: rows n and n + 8
-    int pos[NR], lo[NR];
-    uint32_t qa[KS][NR][2];
-    float sl[NR];
+    // ---- queries (B operand of QK): lane (n, c) holds columns of rows n, n + 8
+    uint32_t qb[KS][NR][2];
+    // of rows 2c, 2c + 1 (+ 8), whose scores the lane gets: score factor, position
+    float sl[NR][2];
+    int pos[NR][2];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const int r = n + 8 * i;
       const int j = r / a.G, h = r - j * a.G;
       const bool ok = r < R;
-      pos[i] = ok ? pos0 + j : -1;
-      lo[i] = a.window > 0 ? max(0, pos[i] - a.window + 1) : 0;
       const uint16_t* qr =
           a.q + (((size_t)b * a.n_tot + (ok ? j : 0)) * a.Hq + g * a.G + (ok ? h : 0)) * D;
-      sl[i] = a.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * i + 2 * c + e;
+        pos[i][e] = row < R ? pos0 + row / a.G : -1;
+        sl[i][e] = a.scale_log2;
+      }
       if constexpr (FMT == kSpanBf16) {
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            qa[k][i][e] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 * e + 2 * c))
+            qb[k][i][e] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 * e + 2 * c))
                              : 0u;
       } else {
         // k-step k of the lane's columns: 4 consecutive ones (2 pairs)
@@ -417,11 +421,11 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
           const int col = FMT == kSpanE4m3 ? 64 * (k >> 2) + 16 * c + 4 * (k & 3)
                                            : (D / 4) * c + 4 * k;
           const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(qr + col)) : make_uint2(0u, 0u);
-          qa[k][i][0] = w.x;
-          qa[k][i][1] = w.y;
+          qb[k][i][0] = w.x;
+          qb[k][i][1] = w.y;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float2 f = bf16x2_to_f2(qa[k][i][e]);
+            const float2 f = bf16x2_to_f2(qb[k][i][e]);
             mq = fmaxf(mq, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
@@ -434,20 +438,28 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float2 f = bf16x2_to_f2(qa[k][i][e]);
+            const float2 f = bf16x2_to_f2(qb[k][i][e]);
             const __half2 hh = __floats2half2_rn(f.x * sc, f.y * sc);
-            qa[k][i][e] = *reinterpret_cast<const uint32_t*>(&hh);
+            qb[k][i][e] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-        sl[i] *= __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int sh2 = __shfl_sync(0xffffffffu, sh, 4 * (2 * c + e));
+          sl[i][e] *= __uint_as_float((uint32_t)(127 - sh2) << 23);
+        }
       }
     }
 
     // m: the rows' reference (log2 units); thr: the raw score that moves it
-    float m[NR], thr[NR], l[NR], acc[NT][4];
+    float m[NR][2], thr[NR][2], l[NR][2], acc[MT][NR][4];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) m[i] = thr[i] = -INFINITY, l[i] = 0.f;
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+      for (int e = 0; e < 2; ++e) m[i][e] = thr[i][e] = -INFINITY, l[i][e] = 0.f;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < NR; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
 
     for (int it = 0; it < count; ++it) {
       __syncwarp();  // every lane is done with the slot that is filled next
@@ -465,167 +477,222 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
         phase ^= 1;
       }
       if ((tag.x & tag.y) == ~0u) continue;  // nothing there
-      // ---- scores: s[t][e] of rows n (e < 2) and n + 8, tokens 8 t + 2c, + 1
-      float s[TT][4];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-      auto qk = [&](int t, int k, uint32_t b0, uint32_t b1) {
-        const uint32_t a1 = NR == 2 ? qa[k][NR - 1][0] : 0u, a3 = NR == 2 ? qa[k][NR - 1][1] : 0u;
-        if constexpr (FMT == kSpanBf16)
-          mma_bf16_16816(s[t], qa[k][0][0], a1, qa[k][0][1], a3, b0, b1);
-        else
-          mma_f16_16816(s[t], qa[k][0][0], a1, qa[k][0][1], a3, b0, b1);
-      };
-      if constexpr (FMT == kSpanBf16) {
-        const int mi = lane >> 3, row = (lane & 7) + 8 * (mi >> 1);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const int ch = (2 * k + (mi & 1)) ^ (row & 7);
-          uint32_t b0, b1, b2, b3;
-          ldmatrix_x4(ks + row * (2 * D) + ch * 16, b0, b1, b2, b3);
-          qk(0, k, b0, b1);
-          qk(1, k, b2, b3);
-        }
-      } else if constexpr (FMT == kSpanE4m3) {
-#pragma unroll
-        for (int k4 = 0; k4 < KS / 4; ++k4)
-#pragma unroll
-          for (int t = 0; t < TT; ++t) {
-            // 16 columns of token 8 t + n
-            const uint4 x = lds128(ks + (n + 8 * t) * D + (c + 4 * k4) * 16);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16(xw[w], b0, b1);
-              qk(t, 4 * k4 + w, b0, b1);
-            }
-          }
-      } else {
-        // D / 4 columns of token 8 t + n: D / 8 bytes, one scale per 16
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const uint32_t row = ks + (t >= 2 ? kc1 : 0u) + (n + 8 * (t & 1)) * (D / 2);
-          const uint32_t scl = ks + (t >= 2 ? ks1 : ks0) + (n + 8 * (t & 1)) * (D / 16);
-          uint32_t xw[D / 32], sx[D / 64];
-          if constexpr (D == 128) {
-            const uint4 x = lds128(row + 16 * c);
-            xw[0] = x.x, xw[1] = x.y, xw[2] = x.z, xw[3] = x.w;
-            const uint32_t u = lds16(scl + 2 * c);
-            sx[0] = __byte_perm(u, 0u, 0x4040) << 7;
-            sx[D / 64 - 1] = __byte_perm(u, 0u, 0x4141) << 7;
-          } else {
-            const uint2 x = lds64(row + 8 * c);
-            xw[0] = x.x, xw[1] = x.y;
-            sx[0] = q4_scale_x2(lds8(scl + c));
-          }
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            uint32_t x[4];
-            q4_unpack8(xw[w], x);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              qk(t, 2 * w + e, hmul2(x[2 * e], sx[w / 2]), hmul2(x[2 * e + 1], sx[w / 2]));
-          }
-        }
-      }
-      // ---- softmax weights
-      // tokens of half 0 and 1: first + 0 .. HT - 1
-      const int ta = (int)tag.x, tb = (int)tag.y;
+      const int ta = (int)tag.x, tb = (int)tag.y;  // first tokens of the halves
       auto half_seen = [&](int t0) {
         return t0 >= 0 && t0 + HT - 1 <= pos0 && (t0 >= lo_last || t0 + HT - 1 < a.sink);
       };
       const bool all_seen = half_seen(ta) && half_seen(tb);
-      auto token = [&](int t, int e) {  // of column 2c + e of tile t (negative: none)
-        const int first = 8 * t < HT ? ta : tb, off = 8 * t - (8 * t < HT ? 0 : HT) + 2 * c + e;
-        return first < 0 ? -1 : first + off;
+      // the unit's token u (negative: absent)
+      auto token = [&](int u) {
+        const int first = u < HT ? ta : tb;
+        return first < 0 ? -1 : first + (u < HT ? u : u - HT);
       };
       if (!all_seen) {
+        // Latents of tokens that no row sees may hold anything, and 0 * NaN
+        // would poison the sums: they (4 bits: their scales) are zeroed here.
+        if (lane < UT) {
+          const int tt = token(lane);
+          if (!(tt >= 0 && tt <= p_last && (tt >= lo_first || tt < a.sink))) {
+            if constexpr (FMT == kSpanQ4) {
+              const uint32_t at = zs + (lane < 16 ? S0 : S1) * RV + (lane & 15) * (RV / 16);
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+              for (int k = 0; k < RV / 16; k += 2)
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + k), "h"((unsigned short)0)
+                             : "memory");
+            } else if constexpr (FMT == kSpanE4m3) {
+              const int F = a.zsplit;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tt = token(t, e & 1), i = NR == 2 ? e >> 1 : 0;
-            if (!(tt >= 0 && tt <= pos[i] && (tt >= lo[i] || tt < a.sink))) s[t][e] = -INFINITY;
+              for (int k = 0; k < RV; k += 16) {
+                const uint32_t at = zs + (k < F ? lane * F + k : 16 * F + lane * (RV - F) + k - F);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u)
+                             : "memory");
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < RV / 8; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 zs + lane * (2 * RV) + 16 * k),
+                             "r"(0u)
+                             : "memory");
+            }
+            if (BULK) fence_proxy_async();  // the slot's next bytes come from the copy engine
+          }
+        }
+        __syncwarp();
+      }
+      // ---- scores: s[v][i] = tokens 16 v + n (e < 2) and + 8, rows 8 i + 2c, + 1
+      float s[VT][NR][4];
+#pragma unroll
+      for (int v = 0; v < VT; ++v)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) s[v][i][0] = s[v][i][1] = s[v][i][2] = s[v][i][3] = 0.f;
+      auto qk = [&](int v, int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          if constexpr (FMT == kSpanBf16)
+            mma_bf16_16816(s[v][i], a0, a1, a2, a3, qb[k][i][0], qb[k][i][1]);
+          else
+            mma_f16_16816(s[v][i], a0, a1, a2, a3, qb[k][i][0], qb[k][i][1]);
+        }
+      };
+      if constexpr (FMT == kSpanBf16) {
+        const int row = lane & 15;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int ch = (2 * k + (lane >> 4)) ^ (row & 7);
+          uint32_t a0, a1, a2, a3;
+          ldmatrix_x4(ks + row * (2 * D) + ch * 16, a0, a1, a2, a3);
+          qk(0, k, a0, a1, a2, a3);
+        }
+      } else if constexpr (FMT == kSpanE4m3) {
+#pragma unroll
+        for (int k4 = 0; k4 < KS / 4; ++k4) {
+          // 16 columns of tokens n and n + 8
+          const uint4 x = lds128(ks + n * D + (c + 4 * k4) * 16);
+          const uint4 y = lds128(ks + (n + 8) * D + (c + 4 * k4) * 16);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16(xw[w], a0, a2);
+            e4m3x4_to_f16(yw[w], a1, a3);
+            qk(0, 4 * k4 + w, a0, a1, a2, a3);
+          }
+        }
+      } else {
+        // D / 4 columns of tokens n and n + 8: D / 8 bytes, one scale per 16
+        const uint32_t kl = ks + lane_k, kls = ks + lane_ks;
+#pragma unroll
+        for (int v = 0; v < VT; ++v) {
+          uint32_t xw[2][D / 32], sx[2][D / 64];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t row = kl + v * H1 * D + y * 8 * (D / 2);
+            const uint32_t scl = kls + (v ? S1 : S0) * D + y * 8 * (D / 16);
+            if constexpr (D == 128) {
+              const uint4 x = lds128(row);
+              xw[y][0] = x.x, xw[y][1] = x.y, xw[y][2] = x.z, xw[y][3] = x.w;
+              const uint32_t u = lds16(scl);
+              sx[y][0] = __byte_perm(u, 0u, 0x4040) << 7;
+              sx[y][D / 64 - 1] = __byte_perm(u, 0u, 0x4141) << 7;
+            } else {
+              const uint2 x = lds64(row);
+              xw[y][0] = x.x, xw[y][1] = x.y;
+              sx[y][0] = q4_scale_x2(lds8(scl));
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {
+            uint32_t x[4], y[4];
+            q4_unpack8(xw[0][w], x);
+            q4_unpack8(xw[1][w], y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              qk(v, 2 * w + e, hmul2(x[2 * e], sx[0][w / 2]), hmul2(y[2 * e], sx[1][w / 2]),
+                 hmul2(x[2 * e + 1], sx[0][w / 2]), hmul2(y[2 * e + 1], sx[1][w / 2]));
+          }
+        }
+      }
+      // ---- softmax weights
+      if (!all_seen) {
+#pragma unroll
+        for (int v = 0; v < VT; ++v)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int tt = token(16 * v + n + 8 * y);
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int p = pos[i][e], lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+                if (!(tt >= 0 && tt <= p && (tt >= lo || tt < a.sink)))
+                  s[v][i][2 * y + e] = -INFINITY;
+              }
           }
       }
       bool grow = false;
-      float mx[NR];
+      float mx[NR][2];
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        mx[i] = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+      for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int t = 1; t < TT; ++t) mx[i] = fmaxf(mx[i], fmaxf(s[t][2 * i], s[t][2 * i + 1]));
-        grow |= mx[i] > thr[i];
-      }
+        for (int e = 0; e < 2; ++e) {
+          mx[i][e] = fmaxf(s[0][i][e], s[0][i][2 + e]);
+#pragma unroll
+          for (int v = 1; v < VT; ++v)
+            mx[i][e] = fmaxf(mx[i][e], fmaxf(s[v][i][e], s[v][i][2 + e]));
+          grow |= mx[i][e] > thr[i][e];
+        }
       if (__any_sync(0xffffffffu, grow)) {
-        float f[NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-          const float mn = fmaxf(m[i], mx[i] * sl[i]);
-          f[i] = mn == -INFINITY ? 1.f : ex2(m[i] - mn);
-          m[i] = mn;
-          thr[i] = (mn + kSpSlack) / sl[i];
-          l[i] *= f[i];
-        }
+          float f[2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          acc[t][0] *= f[0];
-          acc[t][1] *= f[0];
-          acc[t][2] *= f[NR - 1];
-          acc[t][3] *= f[NR - 1];
+          for (int e = 0; e < 2; ++e) {
+            float x = mx[i][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            const float mn = fmaxf(m[i][e], x * sl[i][e]);
+            f[e] = mn == -INFINITY ? 1.f : ex2(m[i][e] - mn);
+            m[i][e] = mn;
+            thr[i][e] = (mn + kSpSlack) / sl[i][e];
+            l[i][e] *= f[e];
+          }
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            acc[t][i][0] *= f[0];
+            acc[t][i][1] *= f[1];
+            acc[t][i][2] *= f[0];
+            acc[t][i][3] *= f[1];
+          }
         }
       }
-      // A operand of PV, k-step v: rows n | n + 8, tokens 16 v + 2c.. | + 8
-      uint32_t pa[TT / 2][4];
+      // B operand of PV: rows n (+ 8 i), tokens 16 v + 2c, + 1 and + 8, + 9
+      uint32_t pb[VT][NR][2], pr[VT][NR][2];  // roundings; remainders (bf16)
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        const float base = m[i] == -INFINITY ? 0.f : m[i];
+        const float base0 = m[i][0] == -INFINITY ? 0.f : m[i][0];
+        const float base1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const float p0 = ex2(fmaf(s[t][2 * i], sl[i], -base));
-          const float p1 = ex2(fmaf(s[t][2 * i + 1], sl[i], -base));
-          l[i] += p0 + p1;
-          if constexpr (FMT == kSpanBf16) {
-            uint32_t hi, rest;
-            split_bf16x2(p0, p1, hi, rest);
-            pa[t / 2][2 * (t & 1) + i] = hi;
-            if (NR == 1) pa[t / 2][2 * (t & 1) + 1] = rest;
-          } else {
-            const __half2 hh = __floats2half2_rn(p0, p1);
-            pa[t / 2][2 * (t & 1) + i] = *reinterpret_cast<const uint32_t*>(&hh);
-            if (NR == 1) pa[t / 2][2 * (t & 1) + 1] = 0u;
-          }
-        }
-      }
-      // ---- latents, 16 tokens a step.  Tokens that no row sees may hold
-      // anything (0 * NaN would poison the sums): they are taken as zeros.
+        for (int v = 0; v < VT; ++v)
 #pragma unroll
-      for (int v = 0; v < TT / 2; ++v) {
-        bool live[4] = {true, true, true, true};  // tokens 2c, 2c + 1, + 8, + 9 of the step
-        if (!all_seen) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tt = token(2 * v + (e >> 1), e & 1);
-            live[e] = tt >= 0 && tt <= p_last && (tt >= lo_first || tt < a.sink);
-          }
-        }
-        if constexpr (FMT == kSpanQ4) {
-          const uint32_t zc = zs + (v ? zc1 : 0u) + 2 * c * (RV / 2);
-          const uint32_t zl = zs + (v ? zs1 : zs0) + 2 * c * (RV / 16);
-          // scale pairs of block k for tokens (2c, 2c + 1) and (+ 8, + 9)
-          auto scales = [&](int k, uint32_t& s01, uint32_t& s89) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[e] = lds8(zl + ((e & 1) + 8 * (e >> 1)) * (RV / 16) + k);
-              if (!all_seen && !live[e]) w[e] = 0;
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = ex2(fmaf(s[v][i][2 * y], sl[i][0], -base0));
+            const float p1 = ex2(fmaf(s[v][i][2 * y + 1], sl[i][1], -base1));
+            l[i][0] += p0;
+            l[i][1] += p1;
+            if constexpr (FMT == kSpanBf16) {
+              uint32_t hi, rest;
+              split_bf16x2(p0, p1, hi, rest);
+              pb[v][i][y] = movmatrix_trans(hi);
+              pr[v][i][y] = movmatrix_trans(rest);
+            } else {
+              const __half2 hh = __floats2half2_rn(p0, p1);
+              pb[v][i][y] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&hh));
             }
-            s01 = __byte_perm(w[0], w[1], 0x5410) << 7;
-            s89 = __byte_perm(w[2], w[3], 0x5410) << 7;
+          }
+      }
+      // ---- latents (A operand of PV), 16 columns and 16 tokens a product
+#pragma unroll
+      for (int v = 0; v < VT; ++v) {
+        auto pv = [&](int t, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            if constexpr (FMT == kSpanBf16) {
+              mma_bf16_16816(acc[t][i], a0, a1, a2, a3, pb[v][i][0], pb[v][i][1]);
+              mma_bf16_16816(acc[t][i], a0, a1, a2, a3, pr[v][i][0], pr[v][i][1]);
+            } else {
+              mma_f16_16816(acc[t][i], a0, a1, a2, a3, pb[v][i][0], pb[v][i][1]);
+            }
+          }
+        };
+        if constexpr (FMT == kSpanQ4) {
+          const uint32_t zl = zs + lane_z + v * H1 * RV, zls = zs + lane_zs + (v ? S1 : S0) * RV;
+          // scale pairs of a block for tokens (2c, 2c + 1) and (+ 8, + 9)
+          auto scales = [&](uint32_t at, uint32_t& s01, uint32_t& s89) {
+            s01 = __byte_perm(lds8(at), lds8(at + RV / 16), 0x5410) << 7;
+            s89 = __byte_perm(lds8(at + 8 * (RV / 16)), lds8(at + 9 * (RV / 16)), 0x5410) << 7;
           };
+          // the 8 columns of two tokens, paired
           auto pairs = [&](uint32_t x0, uint32_t y0, uint32_t (&f)[8]) {
             uint32_t lo4[4], hi4[4];
             q4_unpack8((x0 & 0x0f0f0f0fu) | ((y0 << 4) & 0xf0f0f0f0u), lo4);
@@ -641,68 +708,59 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
             uint32_t x[4], f0[8], f1[8], s01, s89;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              x[e] = lds32(zc + ((e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * w + 4 * n);
+              x[e] = lds32(zl + ((e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * w);
             pairs(x[0], x[1], f0);
             pairs(x[2], x[3], f1);
-            scales(4 * w + (n >> 1), s01, s89);
+            scales(zls + 4 * w, s01, s89);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              mma_f16_16816(acc[8 * w + j], pa[v][0], pa[v][1], pa[v][2], pa[v][3],
-                            hmul2(f0[j], s01), hmul2(f1[j], s89));
+            for (int j = 0; j < 8; j += 2)
+              pv(4 * w + j / 2, hmul2(f0[j], s01), hmul2(f0[j + 1], s01), hmul2(f1[j], s89),
+                 hmul2(f1[j + 1], s89));
           }
-          if constexpr (RV % 64 != 0) {
+          if constexpr (RV % 64 != 0) {  // 32 more columns, 4 a lane
             constexpr int W0 = RV / 64;
             uint32_t x[4], f0[8], f1[8], s01, s89;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              x[e] = lds16(zc + ((e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * W0 + 2 * n);
+              x[e] = lds16(zl - 2 * n + ((e & 1) + 8 * (e >> 1)) * (RV / 2) + 32 * W0);
             pairs(x[0], x[1], f0);
             pairs(x[2], x[3], f1);
-            scales(4 * W0 + (n >> 2), s01, s89);
+            scales(zls - (n >> 1) + (n >> 2) + 4 * W0, s01, s89);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_f16_16816(acc[8 * W0 + j], pa[v][0], pa[v][1], pa[v][2], pa[v][3],
-                            hmul2(f0[j], s01), hmul2(f1[j], s89));
+            for (int j = 0; j < 4; j += 2)
+              pv(4 * W0 + j / 2, hmul2(f0[j], s01), hmul2(f0[j + 1], s01), hmul2(f1[j], s89),
+                 hmul2(f1[j + 1], s89));
+          }
+        } else if constexpr (FMT == kSpanBf16) {
+          // matrices: tokens 0-7 | 8-15 (lanes 16 on) of columns 16 t | + 8
+          const int row = (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            uint32_t a0, a1, a2, a3;
+            ldmatrix_x4_trans(
+                zs + row * (2 * RV) + sp_zchunk<RV>(row, 2 * t + ((lane >> 3) & 1)) * 16, a0, a1,
+                a2, a3);
+            pv(t, a0, a1, a2, a3);
           }
         } else {
-          const uint32_t m0 = (live[0] ? 0xffffu : 0u) | (live[1] ? 0xffff0000u : 0u);
-          const uint32_t m1 = (live[2] ? 0xffffu : 0u) | (live[3] ? 0xffff0000u : 0u);
-          if constexpr (FMT == kSpanBf16) {
-            const int mi = lane >> 3, row = (lane & 7) + 8 * (mi & 1);
+          const int F = a.zsplit;
 #pragma unroll
-            for (int t = 0; t < NT; t += 2) {
-              uint32_t b0, b1, b2, b3;
-              ldmatrix_x4_trans(zs + row * (2 * RV) + sp_zchunk<RV>(row, t + (mi >> 1)) * 16, b0,
-                                b1, b2, b3);
-              if (!all_seen) b0 &= m0, b1 &= m1, b2 &= m0, b3 &= m1;
-              mma_bf16_16816(acc[t], pa[v][0], pa[v][1], pa[v][2], pa[v][3], b0, b1);
-              mma_bf16_16816(acc[t + 1], pa[v][0], pa[v][1], pa[v][2], pa[v][3], b2, b3);
+          for (int w = 0; w < RV / 32; ++w) {
+            const int col = 32 * w + 4 * n;
+            const uint32_t at = zs + (col < F ? col : 16 * F + col - F);
+            const int pitch = col < F ? F : RV - F;
+            uint32_t x[4], f[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = lds32(at + (2 * c + (e & 1) + 8 * (e >> 1)) * pitch);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // token pairs of each column
+              e4m3x4_to_f16(__byte_perm(x[2 * e], x[2 * e + 1], 0x5140), f[e][0], f[e][1]);
+              e4m3x4_to_f16(__byte_perm(x[2 * e], x[2 * e + 1], 0x7362), f[e][2], f[e][3]);
             }
-          } else {
-            const int F = a.zsplit;
 #pragma unroll
-            for (int w = 0; w < RV / 32; ++w) {
-              const int col = 32 * w + 4 * n;
-              const uint32_t at = zs + (col < F ? col : 16 * F + col - F);
-              const int pitch = col < F ? F : RV - F;
-              uint32_t x[4], f[2][4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x[e] = lds32(at + (2 * c + (e & 1) + 8 * (e >> 1)) * pitch);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {  // token pairs of each column
-                e4m3x4_to_f16(__byte_perm(x[2 * e], x[2 * e + 1], 0x5140), f[e][0], f[e][1]);
-                e4m3x4_to_f16(__byte_perm(x[2 * e], x[2 * e + 1], 0x7362), f[e][2], f[e][3]);
-              }
-              if (!all_seen) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[0][j] &= m0, f[1][j] &= m1;
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma_f16_16816(acc[4 * w + j], pa[v][0], pa[v][1], pa[v][2], pa[v][3], f[0][j],
-                              f[1][j]);
-            }
+            for (int j = 0; j < 4; j += 2)
+              pv(2 * w + j / 2, f[0][j], f[0][j + 1], f[1][j], f[1][j + 1]);
           }
         }
       }
@@ -710,21 +768,22 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
 
     // ---- the warps meet
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      float* row = meet + (size_t)(warp * 8 * NR + n + 8 * i) * RS;
-      if (c == 0) {
-        row[0] = m[i];
-        row[1] = l[i];
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
+        float* row = meet + (size_t)(warp * 8 * NR + 8 * i + 2 * c + e) * RS;
+        if (n == 0) {
+          row[0] = m[i][e];
+          row[1] = l[i][e];
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          row[2 + sp_col<FMT, RV>(2 * t, n)] = acc[t][i][e];
+          row[2 + sp_col<FMT, RV>(2 * t + 1, n)] = acc[t][i][2 + e];
+        }
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          row[2 + sp_col<FMT, RV>(t, 2 * c + e)] =
-              NR == 1 && FMT == kSpanBf16 ? acc[t][e] + acc[t][2 + e] : acc[t][2 * i + e];
-    }
     __syncthreads();
     float* part = a.partial + (size_t)(blockIdx.x + bg) * R * RS;
     for (int o = tid; o < R * RV; o += kSpThreads) {
@@ -798,7 +857,7 @@ __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int 
   }
 }
 
-template <int FMT, int D, int RV, int NR>
+template <int FMT, int D, int RV, int NR, bool ONE = false>
 cudaError_t launch_span_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
   constexpr int UT = sp_unit<FMT>();
   // Units of the longest context this call may meet; fewer CTAs when they do
@@ -813,33 +872,33 @@ cudaError_t launch_span_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
   if (grid > kSpanMaxCtas) grid = kSpanMaxCtas;
   if (grid > units / kSpMinUnits) grid = units / kSpMinUnits > 0 ? units / kSpMinUnits : 1;
   constexpr size_t smem = sp_smem<FMT, D, RV, NR>();
-  cudaError_t e = cudaFuncSetAttribute(span_kernel<FMT, D, RV, NR>,
+  cudaError_t e = cudaFuncSetAttribute(span_kernel<FMT, D, RV, NR, ONE>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = launch_k(span_kernel<FMT, D, RV, NR>, dim3((unsigned)grid), dim3(kSpThreads), smem, st, pdl,
+  e = launch_k(span_kernel<FMT, D, RV, NR, ONE>, dim3((unsigned)grid), dim3(kSpThreads), smem, st, pdl,
                a);
   if (e != cudaSuccess) return e;
   return launch_k(span_merge_kernel<UT, RV>, dim3(a.B * a.Hkv), dim3(kSpThreads), 0, st, pdl, a,
                   (int)grid);
 }
 
-template <int FMT>
+template <int FMT, bool ONE = false>
 cudaError_t launch_span_fmt(const SpanArgs& a, cudaStream_t st, bool pdl) {
   const bool two = a.n_tot * a.G > 8;
 #define BKV_SPAN_RV(DD)                                                       \
   switch (a.r_v) {                                                            \
     case 32:                                                                  \
-      return two ? launch_span_t<FMT, DD, 32, 2>(a, st, pdl)                  \
-                 : launch_span_t<FMT, DD, 32, 1>(a, st, pdl);                 \
+      return two ? launch_span_t<FMT, DD, 32, 2, ONE>(a, st, pdl)             \
+                 : launch_span_t<FMT, DD, 32, 1, ONE>(a, st, pdl);            \
     case 64:                                                                  \
-      return two ? launch_span_t<FMT, DD, 64, 2>(a, st, pdl)                  \
-                 : launch_span_t<FMT, DD, 64, 1>(a, st, pdl);                 \
+      return two ? launch_span_t<FMT, DD, 64, 2, ONE>(a, st, pdl)             \
+                 : launch_span_t<FMT, DD, 64, 1, ONE>(a, st, pdl);            \
     case 96:                                                                  \
-      return two ? launch_span_t<FMT, DD, 96, 2>(a, st, pdl)                  \
-                 : launch_span_t<FMT, DD, 96, 1>(a, st, pdl);                 \
+      return two ? launch_span_t<FMT, DD, 96, 2, ONE>(a, st, pdl)             \
+                 : launch_span_t<FMT, DD, 96, 1, ONE>(a, st, pdl);            \
     default:                                                                  \
-      return two ? launch_span_t<FMT, DD, 128, 2>(a, st, pdl)                 \
-                 : launch_span_t<FMT, DD, 128, 1>(a, st, pdl);                \
+      return two ? launch_span_t<FMT, DD, 128, 2, ONE>(a, st, pdl)            \
+                 : launch_span_t<FMT, DD, 128, 1, ONE>(a, st, pdl);           \
   }
   if (a.d == 64) {
     BKV_SPAN_RV(64)
