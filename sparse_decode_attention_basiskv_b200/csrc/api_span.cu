@@ -148,12 +148,13 @@ int basiskv_cache4_write(const basiskv_dims* dims, const basiskv_bf16* k_new,
   a.rows[0] = k_new, a.rows[1] = z_new, a.rows[2] = e_new;
   a.cache[0] = K4, a.cache[1] = Z4, a.cache[2] = E4;
   a.width[0] = dims->d, a.width[1] = dims->r_v, a.width[2] = dims->r_k;
-  for (int i = 0; i < 3; ++i) a.chunks[i] = a.rows[i] ? dims->Hkv * a.width[i] / 8 : 0;
+  for (int i = 0; i < 3; ++i) a.blocks[i] = a.rows[i] ? dims->Hkv * a.width[i] / 16 : 0;
   a.seq_lens = seq_lens;
   const bool in_place = lens_out == seq_lens;
   a.lens_out = in_place ? nullptr : lens_out;
   a.block_table = block_table;
   a.B = dims->B, a.n = n_new, a.Hkv = dims->Hkv, a.S = dims->page_size;
+  a.logS = dims->page_size == 16 ? 4 : 5;
   a.max_pages = dims->max_pages_per_seq, a.num_phys = dims->num_phys_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = status_of(launch_cache4_write(a, st, pdl_allowed()));
@@ -194,11 +195,12 @@ int basiskv_cache4_read(const basiskv_dims* dims, const int32_t* first, int coun
   a.cache[1] = const_cast<uint8_t*>(Z4);
   a.cache[2] = const_cast<uint8_t*>(E4);
   a.width[0] = dims->d, a.width[1] = dims->r_v, a.width[2] = dims->r_k;
-  for (int i = 0; i < 3; ++i) a.chunks[i] = a.out[i] ? dims->Hkv * a.width[i] / 8 : 0;
+  for (int i = 0; i < 3; ++i) a.blocks[i] = a.out[i] ? dims->Hkv * a.width[i] / 16 : 0;
   a.first = first;
   a.seq_lens = seq_lens;
   a.block_table = block_table;
   a.B = dims->B, a.n = count, a.Hkv = dims->Hkv, a.S = dims->page_size;
+  a.logS = dims->page_size == 16 ? 4 : 5;
   a.max_pages = dims->max_pages_per_seq, a.num_phys = dims->num_phys_pages;
   return status_of(launch_cache4_read(a, static_cast<cudaStream_t>(stream), pdl_allowed()));
 }

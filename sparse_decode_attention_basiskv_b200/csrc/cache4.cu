@@ -1,12 +1,13 @@
 // Writing rows into a 4-bit cache, and reading them back.
 //
 // Both are one pass over the data: 2 bytes a column in and 9/16 out, or the
-// other way round, with a few operations a column, so HBM bounds them.  A
-// lane handles 8 columns of one row (a 16-byte access on the dense side and a
-// 4-byte one on the cache side); two neighbouring lanes share a block of 16
-// columns and meet in one shuffle for its largest magnitude.  The columns of
-// all heads of one token's row are contiguous, so a CTA walks tokens with its
-// lanes along that row.
+// other way round, with some five operations a column, so HBM bounds them as
+// long as the bookkeeping stays small.  A thread keeps one block of 16 columns
+// of one head (of the k, z or e row) and walks tokens: 32 contiguous bytes on
+// the dense side (one 256-bit access), 8 bytes of codes and the scale's byte
+// on the cache side, and nothing to share with its neighbours.  The blocks of
+// one token are spread over a CTA's threads, several tokens side by side
+// where a token has few.
 #include "cache4.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -16,136 +17,204 @@ namespace basiskv {
 namespace {
 
 constexpr int kC4Threads = 256;
+constexpr int kC4Batch = 4;  // tokens a thread has in flight
 
-// Where token t of sequence b lives: the tile row index (physical page *
-// S + row), or -1 (no such page).
-__device__ __forceinline__ int c4_row(const Cache4Args& a, int b, int t) {
-  const int p = t / a.S;
-  if (p >= a.max_pages) return -1;
-  const int pp = __ldg(a.block_table + (size_t)b * a.max_pages + p);
-  if (pp < 0 || pp >= a.num_phys) {
-    raise_status(a.status, BASISKV_DEV_BAD_PAGE);
-    return -1;
+struct Block16 {
+  uint32_t w[8];
+};
+// A block of a dense row: one access where the rows are 32-byte aligned, else two.
+__device__ __forceinline__ Block16 ld_block(const uint16_t* p, bool wide) {
+  Block16 v;
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
+                   "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                 : "l"(p));
+  } else {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 y = __ldg(reinterpret_cast<const uint4*>(p + 8));
+    v = {{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
   }
-  return pp * a.S + (t - p * a.S);
+  return v;
+}
+__device__ __forceinline__ void st_block(uint16_t* p, const Block16& v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]),
+                 "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+                 "r"(v.w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    *reinterpret_cast<uint4*>(p + 8) = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+  }
 }
 
-// Part and chunk of task i of one token: the rows of k, z and e one after
-// the other, Hkv * w / 8 chunks each.
-struct C4Task {
+// The thread's block: part (k, z, e), head, block within the head's row.
+struct C4Block {
   int part, g, c, w;
 };
-__device__ __forceinline__ C4Task c4_task(const Cache4Args& a, int i) {
-  C4Task t;
+__device__ __forceinline__ C4Block c4_block(const Cache4Args& a, int i) {
+  C4Block t;
   t.part = 0;
 #pragma unroll
   for (int p = 0; p < 2; ++p)
-    if (t.part == p && i >= a.chunks[p]) {
-      i -= a.chunks[p];
+    if (t.part == p && i >= a.blocks[p]) {
+      i -= a.blocks[p];
       ++t.part;
     }
-  t.w = a.width[t.part];
-  t.g = i / (t.w >> 3);
-  t.c = i - t.g * (t.w >> 3);
+  t.w = t.part == 0 ? a.width[0] : (t.part == 1 ? a.width[1] : a.width[2]);
+  t.g = i / (t.w >> 4);
+  t.c = i - t.g * (t.w >> 4);
   return t;
 }
 
-__global__ void __launch_bounds__(kC4Threads) cache4_write_kernel(Cache4Args a) {
+// Physical page of token t of sequence b, or -1 (out of range: reported).
+__device__ __forceinline__ int c4_page(const Cache4Args& a, int b, int t) {
+  const int p = t >> a.logS;
+  const int pp = p < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + p) : -1;
+  if (pp >= 0 && pp < a.num_phys) return pp;
+  raise_status(a.status, BASISKV_DEV_BAD_PAGE);
+  return -1;
+}
+
+template <bool WRITE>
+__global__ void __launch_bounds__(kC4Threads) cache4_kernel(Cache4Args a, int per, int side) {
   pdl_wait();
   pdl_launch_dependents();
-  const int per = a.chunks[0] + a.chunks[1] + a.chunks[2];  // even: w / 8 is even
   const int b = blockIdx.z;
   const int len = __ldg(a.seq_lens + b);
-  const bool fits = len >= 0 && (long long)len + a.n <= (long long)a.max_pages * a.S;
-  if (a.lens_out && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    if (!fits) raise_status(a.status, BASISKV_DEV_OVERFLOW);
-    a.lens_out[b] = fits ? len + a.n : len;
+  int t0;  // token of row 0
+  if constexpr (WRITE) {
+    const bool fits = len >= 0 && (long long)len + a.n <= (long long)a.max_pages * a.S;
+    if (a.lens_out && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+      if (!fits) raise_status(a.status, BASISKV_DEV_OVERFLOW);
+      a.lens_out[b] = fits ? len + a.n : len;
+    }
+    if (!fits) return;
+    t0 = len;
+  } else {
+    t0 = __ldg(a.first + b);
   }
-  if (!fits) return;
-  for (int j = blockIdx.y; j < a.n; j += gridDim.y) {
-    const int row = c4_row(a, b, len + j);
-    if (row < 0) continue;
-    const int pp = row / a.S, r = row - pp * a.S;
-    for (int i = blockIdx.x * kC4Threads + threadIdx.x; i < per; i += gridDim.x * kC4Threads) {
-      const C4Task t = c4_task(a, i);
-      const uint16_t* src = a.rows[t.part];
-      const uint4 v = ldg_stream(src + (((size_t)b * a.n + j) * a.Hkv + t.g) * t.w + 8 * t.c);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      float f[8], m = 0.f;
+  const int s = threadIdx.x / per, i = blockIdx.x * kC4Threads + threadIdx.x - s * per;
+  if (s >= side || i >= a.blocks[0] + a.blocks[1] + a.blocks[2]) return;
+  const C4Block t = c4_block(a, i);
+  // dense rows, and the block's place in a tile
+  const size_t pitch = (size_t)a.Hkv * t.w;
+  const size_t dense = (size_t)b * a.n * pitch + t.g * t.w + 16 * t.c;
+  const uint16_t* src =
+      WRITE ? (t.part == 0 ? a.rows[0] : t.part == 1 ? a.rows[1] : a.rows[2]) + dense : nullptr;
+  uint16_t* dst =
+      WRITE ? nullptr : (t.part == 0 ? a.out[0] : t.part == 1 ? a.out[1] : a.out[2]) + dense;
+  const bool wide = (reinterpret_cast<uintptr_t>(WRITE ? src : dst) & 31) == 0;
+  const uint32_t tile_bytes = q4_tile_bytes(a.S, t.w);
+  uint8_t* cache = (t.part == 0 ? a.cache[0] : t.part == 1 ? a.cache[1] : a.cache[2]) +
+                   (size_t)t.g * tile_bytes;
+  const size_t page_bytes = (size_t)a.Hkv * tile_bytes;
+  const uint32_t code_at = 8 * t.c, scale_at = (a.S * t.w >> 1) + t.c;
+
+  const int step = side * gridDim.y;
+  for (int j0 = blockIdx.y * side + s; j0 < a.n; j0 += kC4Batch * step) {
+    if constexpr (WRITE) {
+      Block16 v[kC4Batch];
+      int pp[kC4Batch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[2 * k] = bf16lo(u[k]);
-        f[2 * k + 1] = bf16hi(u[k]);
-        m = fmaxf(m, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+      for (int k = 0; k < kC4Batch; ++k) {
+        const int j = j0 + k * step;
+        pp[k] = -1;
+        if (j < a.n) {
+          v[k] = ld_block(src + (size_t)j * pitch, wide);
+          pp[k] = c4_page(a, b, t0 + j);
+        }
       }
-      // lanes 2i and 2i + 1 hold one block and leave the loop together
-      const unsigned pair = 3u << (threadIdx.x & 30);
-      m = fmaxf(m, __shfl_xor_sync(pair, m, 1));
-      const uint32_t sb = q4_scale_byte(m);
-      const float s = q4_scale_value(sb);
-      uint32_t codes = 0;
-      if (sb) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          codes |= q4_pack2(__fdiv_rn(f[2 * k], s), __fdiv_rn(f[2 * k + 1], s)) << (8 * k);
+      for (int k = 0; k < kC4Batch; ++k) {
+        if (pp[k] < 0) continue;
+        // largest magnitude on pairs of bf16 without their signs (integer order)
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = __vmaxu2(m, v[k].w[e] & 0x7fff7fffu);
+        const float amax = __uint_as_float(max(m & 0xffff0000u, m << 16));
+        const uint32_t sb = q4_scale_byte(amax);
+        uint2 codes = make_uint2(0u, 0u);
+        if (sb) {
+          float r;
+          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(q4_scale_value(sb)));
+          const float2 inv = make_float2(r, r);
+          float2 x[4], y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = q4_quotient2(bf16x2_to_f2(v[k].w[e]), inv);
+            y[e] = q4_quotient2(bf16x2_to_f2(v[k].w[4 + e]), inv);
+          }
+          codes = make_uint2(q4_pack8(x), q4_pack8(y));
+        }
+        const int r = (t0 + j0 + k * step) & (a.S - 1);
+        uint8_t* tile = cache + pp[k] * page_bytes;
+        *reinterpret_cast<uint2*>(tile + r * (t.w >> 1) + code_at) = codes;
+        tile[r * (t.w >> 4) + scale_at] = (uint8_t)sb;
       }
-      uint8_t* tile = a.cache[t.part] + (size_t)(pp * a.Hkv + t.g) * q4_tile_bytes(a.S, t.w);
-      *reinterpret_cast<uint32_t*>(tile + (r * t.w >> 1) + 4 * t.c) = codes;
-      if (!(t.c & 1)) tile[(a.S * t.w >> 1) + (r * t.w >> 4) + (t.c >> 1)] = (uint8_t)sb;
+    } else {
+      uint2 w[kC4Batch];
+      uint32_t sb[kC4Batch];
+      bool ok[kC4Batch];
+#pragma unroll
+      for (int k = 0; k < kC4Batch; ++k) {
+        const int j = j0 + k * step;
+        const long long tok = (long long)t0 + j;
+        ok[k] = j < a.n && tok >= 0 && tok < len;  // else the row is left as it was
+        if (!ok[k]) continue;
+        const int pp = c4_page(a, b, (int)tok);
+        ok[k] = pp >= 0;
+        if (!ok[k]) continue;
+        const uint8_t* tile = cache + pp * page_bytes;
+        const int r = (int)tok & (a.S - 1);
+        w[k] = __ldg(reinterpret_cast<const uint2*>(tile + r * (t.w >> 1) + code_at));
+        sb[k] = __ldg(tile + r * (t.w >> 4) + scale_at);
+      }
+#pragma unroll
+      for (int k = 0; k < kC4Batch; ++k) {
+        if (!ok[k]) continue;
+        const uint32_t s2 = q4_scale_x2(sb[k]);
+        uint32_t h[8];
+        q4_unpack8(w[k].x, *reinterpret_cast<uint32_t(*)[4]>(h));
+        q4_unpack8(w[k].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+        Block16 o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // exact in f16 and in bf16
+          const uint32_t p = hmul2(h[e], s2);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+          const __nv_bfloat162 u = __floats2bfloat162_rn(f.x, f.y);
+          o.w[e] = *reinterpret_cast<const uint32_t*>(&u);
+        }
+        st_block(dst + (size_t)(j0 + k * step) * pitch, o, wide);
+      }
     }
   }
 }
 
-__global__ void __launch_bounds__(kC4Threads) cache4_read_kernel(Cache4Args a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int per = a.chunks[0] + a.chunks[1] + a.chunks[2];
-  const int b = blockIdx.z;
-  const int first = __ldg(a.first + b);
-  const int len = __ldg(a.seq_lens + b);
-  for (int j = blockIdx.y; j < a.n; j += gridDim.y) {
-    const long long t64 = (long long)first + j;
-    if (t64 < 0 || t64 >= len) continue;  // not a live token: its row is left as it was
-    const int row = c4_row(a, b, (int)t64);
-    if (row < 0) continue;
-    const int pp = row / a.S, r = row - pp * a.S;
-    for (int i = blockIdx.x * kC4Threads + threadIdx.x; i < per; i += gridDim.x * kC4Threads) {
-      const C4Task t = c4_task(a, i);
-      const uint8_t* tile =
-          a.cache[t.part] + (size_t)(pp * a.Hkv + t.g) * q4_tile_bytes(a.S, t.w);
-      const uint32_t w =
-          __ldg(reinterpret_cast<const uint32_t*>(tile + (r * t.w >> 1) + 4 * t.c));
-      const float s = q4_scale_value(__ldg(tile + (a.S * t.w >> 1) + (r * t.w >> 4) + (t.c >> 1)));
-      uint32_t h[4], o[4];
-      q4_unpack8(w, h);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-        o[k] = (uint32_t)f_to_bf16(f.x * s) | ((uint32_t)f_to_bf16(f.y * s) << 16);
-      }
-      *reinterpret_cast<uint4*>(a.out[t.part] + (((size_t)b * a.n + j) * a.Hkv + t.g) * t.w +
-                                8 * t.c) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
-}
-
-dim3 c4_grid(const Cache4Args& a) {
-  const int per = a.chunks[0] + a.chunks[1] + a.chunks[2];
-  const int gx = (per + kC4Threads - 1) / kC4Threads;
-  long gy = (long)num_sms() * 16 / ((long)gx * a.B);
+template <bool WRITE>
+cudaError_t launch_cache4(const Cache4Args& a, cudaStream_t st, bool pdl) {
+  const int all = a.blocks[0] + a.blocks[1] + a.blocks[2];
+  const int per = all < kC4Threads ? all : kC4Threads;  // threads a token and CTA
+  const int side = kC4Threads / per;                    // tokens side by side
+  const int gx = (all + per - 1) / per;
+  // CTAs along the tokens: 8 resident ones an SM twice over, none without a token
+  long long gy = (long long)num_sms() * 16 / ((long long)gx * a.B);
+  const long long most = (a.n + side - 1) / side;
+  if (gy > most) gy = most;
   if (gy < 1) gy = 1;
-  if (gy > a.n) gy = a.n;
-  return dim3(gx, (unsigned)gy, a.B);
+  return launch_k(cache4_kernel<WRITE>, dim3(gx, (unsigned)gy, a.B), dim3(kC4Threads), 0, st, pdl,
+                  a, per, side);
 }
 
 }  // namespace
 
 cudaError_t launch_cache4_write(const Cache4Args& a, cudaStream_t st, bool pdl) {
-  return launch_k(cache4_write_kernel, c4_grid(a), dim3(kC4Threads), 0, st, pdl, a);
+  return launch_cache4<true>(a, st, pdl);
 }
 
 cudaError_t launch_cache4_read(const Cache4Args& a, cudaStream_t st, bool pdl) {
-  return launch_k(cache4_read_kernel, c4_grid(a), dim3(kC4Threads), 0, st, pdl, a);
+  return launch_cache4<false>(a, st, pdl);
 }
 
 }  // namespace basiskv

@@ -240,12 +240,12 @@ struct Cache4Args {
   const uint16_t* rows[3];  // write: k, z, e rows [B][n][Hkv][w] bf16
   uint16_t* out[3];         // read: the same layout
   uint8_t* cache[3];        // 4-bit tiles (cache4.cuh)
-  int width[3], chunks[3];  // w, and Hkv * w / 8 (0: the part is absent)
+  int width[3], blocks[3];  // w, and Hkv * w / 16 (0: the part is absent)
   const int32_t* seq_lens;
   const int32_t* first;  // read: first token of each sequence
   int32_t* lens_out;     // write: lengths after it (null: not written here)
   const int32_t* block_table;
-  int B, n, Hkv, S, max_pages, num_phys;
+  int B, n, Hkv, S, logS, max_pages, num_phys;
   unsigned int* status;
 };
 cudaError_t launch_cache4_write(const Cache4Args& a, cudaStream_t st, bool pdl);
