@@ -34,9 +34,10 @@
 // columns of neighbouring tokens and pairs them); the scores, [token][row],
 // become PV's B operand with one 8x8 transposition per 8 tokens.
 //
-// The running maximum moves only when a score passes it by 8 (a factor of
-// 256 in the weights, far inside the range of f16): then the warp takes the
-// rows' maxima over their lanes and rescales; all other units cost one vote.
+// The running reference moves only when a score passes it by a wide margin
+// (2^15 or 2^64 in the weights, which the operands' types hold): then the warp
+// takes the rows' maxima over their lanes and rescales; all other units cost
+// one vote.
 //
 // Precision: scores and sums in fp32.  The weights of PV are rounded to f16
 // (2^-12 of each weight, an eighth of the output's own rounding) where the
@@ -59,7 +60,13 @@ namespace {
 
 constexpr int kSpThreads = kLineMaxSeqs;  // a thread scans a sequence's length
 constexpr int kSpWarps = kSpThreads / 32;
-constexpr float kSpSlack = 8.f;
+// How far (log2) scores may pass the reference before it moves: the weights then
+// reach 2^15 in f16, 2^64 in bf16, whose products and sums stay far inside
+// fp32's range, at the same relative precision.
+template <int FMT>
+constexpr float sp_slack() {
+  return FMT == kSpanBf16 ? 64.f : 15.f;
+}
 
 // Tokens of a unit.
 template <int FMT>
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
             const float mn = fmaxf(m[i][e], x * sl[i][e]);
             f[e] = mn == -INFINITY ? 1.f : ex2(m[i][e] - mn);
             m[i][e] = mn;
-            thr[i][e] = (mn + kSpSlack) / sl[i][e];
+            thr[i][e] = (mn + sp_slack<FMT>()) / sl[i][e];
             l[i][e] *= f[e];
           }
 #pragma unroll

@@ -15,14 +15,16 @@
 // exponentials a KV tile: at d 128, r_v 64 the tensor cores need about 1540
 // clocks and the 16 exponentials a clock 2048, so the exponentials bound it.
 //
-// Roles (16 warps, one CTA an SM): warps 0-3 and 4-7 hold the softmax of one
-// row tile each, a thread a row (no shuffles), and rescale O, seldom: the
-// reference maximum moves only when the row's maximum has passed it by 8 in
-// log2; warps 8-11 bring in the KV tiles page by page into the swizzled layout
-// (bf16 by cp.async; E4M3 and 4-bit rows widened to f16 on the way, exactly);
-// one thread of warp 12 issues the MMAs, row tile 1's while row tile 0's
-// softmax runs and the other way round.  Tensor memory: S 2 x 128 columns (P
-// over the first 64 of each), O 2 x 128.
+// Roles (13 warps, one CTA an SM): warps 0-3 and 4-7 hold the softmax of one
+// row tile each, a thread a row (no shuffles).  The weights are taken against
+// the reference maximum at hand in one pass over S, which also finds the tile's
+// maximum; only where a row's has passed the reference by a wide margin does the
+// warp move it, rescale O and take the pass again.  Warps 8-11 bring in the KV
+// tiles page by page into the swizzled layout (bf16 by cp.async; E4M3 and
+// 4-bit rows widened to f16 on the way, exactly), a tile ahead of what they
+// hand over; warp 12 issues the MMAs, row tile 1's while row tile 0's softmax
+// runs and the other way round.  Tensor memory: S 2 x 128 columns (P over the
+// first 64 of each), O 2 x 128.
 //
 // Few items: the KV tiles of an item are cut into nsplit runs, whose partial
 // sums span_tc_merge_kernel joins.
@@ -37,9 +39,15 @@
 namespace basiskv {
 namespace {
 
-constexpr int kTcThreads = 512;
+constexpr int kTcThreads = 416;
 constexpr int kTcRows = 256;  // two row tiles
-constexpr float kTcSlack = 8.f;
+// How far (log2) scores may pass the reference before it moves: the weights then
+// reach 2^15 in f16, 2^64 in bf16, whose products and sums stay far inside
+// fp32's range, at the same relative precision.
+template <int FMT>
+constexpr float tc_slack() {
+  return FMT == kSpanBf16 ? 64.f : 15.f;
+}
 
 template <int D, int RV>
 struct TcGeom {
@@ -116,7 +124,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
   __shared__ float row_scale[kTcRows];
   uint64_t *kfull = bars, *kempty = bars + NST, *zfull = bars + 2 * NST, *zempty = bars + 3 * NST;
   uint64_t *sfull = bars + 4 * NST, *pfull = sfull + 2, *ofull = sfull + 4;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const uint32_t sq = smem_u32(smem), sk = sq + Gm::kQBytes, sz = sk + NST * Gm::kKBytes;
 
   if (tid == 0) {
@@ -198,52 +207,63 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
   const uint32_t tmem = tmem_slot;
   volatile int* abrt = &abort_flag;
 
-  if (warp >= 12) {
+  if (warp == 12) {
     // ------------------------------------------------------------ MMA issue
-    if (tid == 12 * 32 && n > 0) {
+    if (n > 0) {
       constexpr uint32_t id_qk = tc_idesc(128, 128, BF, false);
       constexpr uint32_t id_pv = tc_idesc(128, RV, BF, true);
-      auto qk = [&](int t, int i) {
-        const uint32_t qb = sq + t * (Gm::kQBytes / 2), kb = sk + (i % NST) * Gm::kKBytes;
+      const uint64_t dq = tc_sdesc(sq), dk = tc_sdesc(sk), dz = tc_sdesc(sz, 16384);
+      const bool lead = elect_one();
+      auto qk = [&](int t, int stage) {
+        const uint64_t q = dq + t * (Gm::kQBytes / 2 >> 4), k0 = dk + stage * (Gm::kKBytes >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc_mma_ss(tmem + 128 * t, tc_sdesc(qb + (k >> 2) * 16384 + (k & 3) * 32),
-                    tc_sdesc(kb + (k >> 2) * 16384 + (k & 3) * 32), id_qk, k > 0);
+          tc_mma_ss(tmem + 128 * t, q + (k >> 2) * 1024 + (k & 3) * 2,
+                    k0 + (k >> 2) * 1024 + (k & 3) * 2, id_qk, k > 0);
         tc_commit_to(&sfull[t]);
       };
-      auto pv = [&](int t, int i) {
-        const uint32_t zb = sz + (i % NST) * Gm::kZBytes;
+      auto pv = [&](int t, int stage, bool first) {
+        const uint64_t z = dz + stage * (Gm::kZBytes >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, tc_sdesc(zb + k * 2048, 16384),
-                    id_pv, i > 0 || k > 0);
+          tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, z + k * 128, id_pv,
+                    !first || k > 0);
         tc_commit_to(&ofull[t]);
       };
       bool ok = mbar_wait_or_abort(&kfull[0], 0, a.status, abrt);
       if (ok) {
         tc_fence_after_sync();
-        for (int t = 0; t < nt; ++t) qk(t, 0);
-        tc_commit_to(&kempty[0]);
+        if (lead) {
+          qk(0, 0);
+          if (nt == 2) qk(1, 0);
+          tc_commit_to(&kempty[0]);
+        }
       }
+      int st = 0, st_ph = 0;  // ring stage of tile i and its turn
       for (int i = 0; ok && i < n; ++i) {
+        const int nx = st + 1 == NST ? 0 : st + 1, nx_ph = st_ph ^ (nx == 0);
         for (int t = 0; ok && t < nt; ++t) {
-          ok = mbar_wait_or_abort(&pfull[t], i & 1, a.status, abrt);
-          if (ok && t == 0)
-            ok = mbar_wait_or_abort(&zfull[i % NST], (i / NST) & 1, a.status, abrt);
-          if (!ok) break;
+          if (t == 0) {
+            ok = mbar_wait_or_abort(&zfull[st], st_ph, a.status, abrt);
+            if (ok && i + 1 < n) ok = mbar_wait_or_abort(&kfull[nx], nx_ph, a.status, abrt);
+          }
+          if (ok) ok = mbar_wait_or_abort(&pfull[t], i & 1, a.status, abrt);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
           tc_fence_after_sync();
-          pv(t, i);
-          if (t == nt - 1) tc_commit_to(&zempty[i % NST]);
-          if (i + 1 < n) {
-            if (t == 0) {
-              ok = mbar_wait_or_abort(&kfull[(i + 1) % NST], ((i + 1) / NST) & 1, a.status, abrt);
-              if (!ok) break;
-              tc_fence_after_sync();
+          if (lead) {
+            pv(t, st, i == 0);
+            if (t == nt - 1) tc_commit_to(&zempty[st]);
+            if (i + 1 < n) {
+              qk(t, nx);
+              if (t == nt - 1) tc_commit_to(&kempty[nx]);
             }
-            qk(t, i + 1);
-            if (t == nt - 1) tc_commit_to(&kempty[(i + 1) % NST]);
           }
         }
+        st = nx;
+        st_ph = nx_ph;
       }
     }
   } else if (warp >= 8) {
@@ -290,42 +310,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
           cp_async16_or_zero(dst + tc_off(32 * w + r, c), a.Z + off, tr >= 0);
         }
       };
-      // groups in flight: K_0, Z_0, K_1, Z_1, ...; a tile's arrival follows
-      // the next copy's issue
+      // groups in flight: K_0, Z_0, K_1, Z_1, ...; a part is handed over when
+      // the next tile's has been requested
       int row = n > 0 ? tile_row(tc_tile(it, i0) * 128 + lt) : -1;
+      bool ok = true;
       for (int i = 0; i < n; ++i) {
-        const int next =
-            i + 1 < n ? tile_row(tc_tile(it, i0 + i + 1) * 128 + lt) : -1;
-        if (i >= NST &&
-            !mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
-          break;
+        const int next = i + 1 < n ? tile_row(tc_tile(it, i0 + i + 1) * 128 + lt) : -1;
+        if (i >= NST) ok = mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!__all_sync(0xffffffffu, ok)) break;
         copy_k(i, row);
         cp_async_commit();
         if (i > 0) {
-          cp_async_wait_group<1>();
+          cp_async_wait_group<2>();
+          fence_proxy_async();
+          mbar_arrive(&kfull[(i - 1) % NST]);
+        }
+        if (i >= NST) ok = mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        copy_z(i, row);
+        cp_async_commit();
+        if (i > 0) {
+          cp_async_wait_group<2>();
           fence_proxy_async();
           mbar_arrive(&zfull[(i - 1) % NST]);
         }
-        if (i >= NST &&
-            !mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
-          break;
-        copy_z(i, row);
-        cp_async_commit();
-        cp_async_wait_group<1>();
-        fence_proxy_async();
-        mbar_arrive(&kfull[i % NST]);
         row = next;
       }
       cp_async_wait_all();
       fence_proxy_async();
-      if (n > 0 && !*abrt) mbar_arrive(&zfull[(n - 1) % NST]);
+      if (n > 0 && ok) {
+        mbar_arrive(&kfull[(n - 1) % NST]);
+        mbar_arrive(&zfull[(n - 1) % NST]);
+      }
     } else {
-      // A thread widens one row of each tile; the next part's bytes are
-      // requested before the current one is converted.
+      // A thread widens one row of each tile; the next tile's bytes are
+      // requested before the current ones are converted, and its place in the
+      // cache was looked up a tile earlier.
       constexpr int KW = FMT == kSpanQ4 ? D / 8 : D / 4;    // 32-bit words of codes a row
       constexpr int ZW = FMT == kSpanQ4 ? RV / 8 : RV / 4;
       constexpr int KS = D / 64, ZS = (RV / 16 + 3) / 4;    // words of scales (4 bits only)
-      uint32_t kw[KW], zw[ZW], ks[KS > 0 ? KS : 1], zs[ZS];
       auto load = [&](const uint8_t* base, int row, int wdt, uint32_t* dst, int nw, uint32_t* sc,
                       bool z) {
         if (row < 0) return;
@@ -378,25 +401,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
           sts128(dst + tc_off(lt, c), o[0], o[1], o[2], o[3]);
         }
       };
-      int row = n > 0 ? tile_row(tc_tile(it, i0) * 128 + lt) : -1;
-      if (n > 0) load(a.K, row, D, kw, KW, ks, false);
-      for (int i = 0; i < n; ++i) {
-        load(a.Z, row, RV, zw, ZW, zs, true);
-        const int next = i + 1 < n ? tile_row(tc_tile(it, i0 + i + 1) * 128 + lt) : -1;
-        if (i >= NST &&
-            !mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
-          break;
-        put(sk + (i % NST) * Gm::kKBytes, row >= 0, kw, D, ks);
+      struct Raw {
+        int row;
+        uint32_t kw[KW], zw[ZW], ks[KS], zs[ZS];
+      };
+      auto place = [&](int i) { return i < n ? tile_row(tc_tile(it, i0 + i) * 128 + lt) : -1; };
+      auto fetch = [&](Raw& x, int row) {
+        x.row = row;
+        load(a.K, row, D, x.kw, KW, x.ks, false);
+        load(a.Z, row, RV, x.zw, ZW, x.zs, true);
+      };
+      bool ok = true;
+      auto hand_over = [&](const Raw& x, int i) {
+        if (i >= NST) ok = mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        put(sk + (i % NST) * Gm::kKBytes, x.row >= 0, x.kw, D, x.ks);
         fence_proxy_async();
         mbar_arrive(&kfull[i % NST]);
-        if (i + 1 < n) load(a.K, next, D, kw, KW, ks, false);
-        if (i >= NST &&
-            !mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt))
-          break;
-        put(sz + (i % NST) * Gm::kZBytes, row >= 0, zw, RV, zs);
+        if (i >= NST) ok = mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        put(sz + (i % NST) * Gm::kZBytes, x.row >= 0, x.zw, RV, x.zs);
         fence_proxy_async();
         mbar_arrive(&zfull[i % NST]);
-        row = next;
+        return true;
+      };
+      Raw x0, x1;
+      fetch(x0, place(0));
+      int next = place(1);
+      for (int i = 0; i < n; i += 2) {
+        fetch(x1, next);
+        next = place(i + 2);
+        if (!hand_over(x0, i) || i + 1 == n) break;
+        fetch(x0, next);
+        next = place(i + 3);
+        if (!hand_over(x1, i + 1)) break;
       }
     }
   } else {
@@ -421,88 +459,97 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
         tc_fence_after_sync();
         const int t0 = tc_tile(it, i0 + i) * 128;
         const bool masked = !(t0 + 127 <= pos_a && (t0 >= lo_b || t0 + 127 < a.sink));
-        // column x holds token t0 + x: visible up to pos, from lo on or below
-        // the sinks' end
-        const int me = pos - t0, mf = lo - t0, mg = a.sink - t0;
-        auto mask32 = [&](uint32_t (&s)[32], int x0) {
+        uint32_t sa[16], sb[16], p[64];
+        if (masked) {
+          // column x holds token t0 + x: visible up to pos, from lo on or below
+          // the sinks' end; the others become -inf in place
+          const int me = pos - t0, mf = lo - t0, mg = a.sink - t0;
+#pragma unroll 1
+          for (int x0 = 0; x0 < 128; x0 += 32) {
+            tc_ld32(ts + x0, p);
+            tc_wait_ld(p);
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (x0 + x > me || (x0 + x < mf && x0 + x >= mg)) s[x] = 0xff800000u;
-        };
-        uint32_t sa[32], sb[32];
-        float mx = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 128; x += 64) {
-          tc_ld32(ts + x, sa);
-          tc_ld32(ts + x + 32, sb);
-          tc_wait_ld();
-          if (masked) {
-            mask32(sa, x);
-            mask32(sb, x + 32);
+            for (int x = 0; x < 32; ++x)
+              if (x0 + x > me || (x0 + x < mf && x0 + x >= mg)) p[x] = 0xff800000u;
+            tc_st32(ts + x0, p);
           }
-#pragma unroll
-          for (int y = 0; y < 32; ++y)
-            mx = fmaxf(mx, fmaxf(__uint_as_float(sa[y]), __uint_as_float(sb[y])));
+          tc_wait_st();
         }
-        mx *= sl;
-        if (i == 0) {
-          m = mx;
-        } else {
-          const bool grow = mx > m + kTcSlack;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2(m - mx) : 1.f;
-            if (grow) m = mx;
-            l *= f;
-            ok = mbar_wait_or_abort(&ofull[t], (i - 1) & 1, a.status, abrt);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after_sync();
+        auto max16 = [&](const uint32_t (&s)[16], float v) {
 #pragma unroll
-            for (int x = 0; x < RV / 32; ++x) {
-              uint32_t o[32];
-              tc_ld32(to + 32 * x, o);
-              tc_wait_ld();
+          for (int x = 0; x < 16; x += 2)
+            v = fmaxf(v, fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
+          return v;
+        };
+        if (i == 0) {  // the first tile sets the reference
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int x = 0; x < 128; x += 16) {
+            tc_ld16(ts + x, sa);
+            tc_wait_ld16(sa);
+            mx = max16(sa, mx);
+          }
+          m = mx * sl;
+        }
+        float sum0, sum1;
+        for (;;) {
+          const float base = m == -INFINITY ? 0.f : m;
+          float mx = -INFINITY;
+          sum0 = sum1 = 0.f;
+          // (scalar products: the packed two-lane forms measured slower here)
+          auto weights = [&](uint32_t (&s)[16], int x) {
+            mx = max16(s, mx);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tc_st32(to + 32 * x, o);
+            for (int y = 0; y < 16; y += 2) {
+              const float p0 = ex2(fmaf(__uint_as_float(s[y]), sl, -base));
+              const float p1 = ex2(fmaf(__uint_as_float(s[y + 1]), sl, -base));
+              sum0 += p0;
+              sum1 += p1;
+              if constexpr (BF) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+                p[(x + y) / 2] = *reinterpret_cast<const uint32_t*>(&v);
+              } else {
+                const __half2 v = __floats2half2_rn(p0, p1);
+                p[(x + y) / 2] = *reinterpret_cast<const uint32_t*>(&v);
+              }
             }
+            // done with these scores before the next ones come
+            asm volatile("" : "+f"(mx), "+f"(sum0), "+f"(sum1));
+          };
+          tc_ld16(ts, sa);
+          tc_wait_ld16(sa);
+#pragma unroll
+          for (int x = 0; x < 128; x += 32) {
+            tc_ld16(ts + x + 16, sb);
+            weights(sa, x);
+            tc_wait_ld16(sb);
+            if (x + 32 < 128) tc_ld16(ts + x + 32, sa);
+            weights(sb, x + 16);
+            if (x + 32 < 128) tc_wait_ld16(sa);
+          }
+          mx *= sl;
+          const bool grow = mx > m + tc_slack<FMT>();
+          if (!__any_sync(0xffffffffu, grow)) break;
+          // (not at i = 0, where the reference is the maximum)
+          const float f = grow ? ex2(m - mx) : 1.f;
+          if (grow) m = mx;
+          l *= f;
+          ok = i > 0 ? mbar_wait_or_abort(&ofull[t], (i - 1) & 1, a.status, abrt) : ok;
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int x = 0; x < RV / 32; ++x) {  // p is free here: the pass is taken again
+            tc_ld32(to + 32 * x, p);
+            tc_wait_ld(p);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) p[y] = __float_as_uint(__uint_as_float(p[y]) * f);
+            tc_st32(to + 32 * x, p);
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;
-        float sum0 = 0.f, sum1 = 0.f;
-        // The scores are read a second time rather than held (128 registers a
-        // thread).  P of columns x .. x + 31 goes over columns x / 2 .. of S,
-        // which were read before.
-        auto weights = [&](uint32_t (&s)[32], int x) {
-          if (masked) mask32(s, x);
-          uint32_t p[16];
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[y]), sl, -base));
-            const float p1 = ex2(fmaf(__uint_as_float(s[y + 1]), sl, -base));
-            sum0 += p0;
-            sum1 += p1;
-            if constexpr (BF) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
-              p[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
-            } else {
-              const __half2 v = __floats2half2_rn(p0, p1);
-              p[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-          }
-          tc_st16(ts + x / 2, p);
-        };
-        tc_ld32(ts, sa);
-        tc_wait_ld();
-        tc_ld32(ts + 32, sb);
-        weights(sa, 0);
-        tc_wait_ld();
-        tc_ld32(ts + 64, sa);
-        weights(sb, 32);
-        tc_wait_ld();
-        tc_ld32(ts + 96, sb);
-        weights(sa, 64);
-        tc_wait_ld();
-        weights(sb, 96);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        // P over the first 64 columns of S, which every lane has read
+        tc_st32(ts, p);
+        tc_st32(ts + 32, p + 32);
         l += sum0 + sum1;
         tc_wait_st();
         tc_fence_before_sync();
@@ -523,7 +570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
           uint32_t o[32];
           if (n > 0) {
             tc_ld32(to + 32 * x, o);
-            tc_wait_ld();
+            tc_wait_ld(o);
           } else {
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = 0u;
