@@ -276,7 +276,7 @@ struct SpanArgs {
   const int32_t* sel;  // [B][Hkv][top_k] or null
   float* partial;      // span_slots() * rows * (r_v + 2) floats
   uint16_t* out;       // [B][n_tot][Hq][r_v] bf16
-  int B, Hq, Hkv, G, d, r_v, S, logS, max_pages, num_phys, max_seq_len, top_k;
+  int B, Hq, Hkv, G, logG, d, r_v, S, logS, max_pages, num_phys, max_seq_len, top_k;
   int n_tot;  // query tokens per sequence, the last at position seq_lens[b] - 1
   int sink, window;  // window 0: everything
   int zsplit;
@@ -293,23 +293,15 @@ cudaError_t launch_span_e4m3(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_q4(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_q4_p32(const SpanArgs& a, cudaStream_t st, bool pdl);
 
-// Prompt form (tensor cores; no selection): work items
-// of two row tiles, each cut into nsplit runs of KV tiles while the items
-// alone would leave SMs idle.
-inline int span_tc_items(int B, int Hkv, int G, int n_tot) {
-  const int tq2 = 256 / G;
-  return B * Hkv * ((n_tot + tq2 - 1) / tq2);
-}
-inline int span_tc_splits(int items, int n_tot, int max_seq_len, int sink, int window) {
-  long long span = max_seq_len;
-  if (window > 0 && (long long)window + n_tot + sink < span) span = window + n_tot + sink;
-  long long most = span / 512 > 0 ? span / 512 : 1;  // at least 4 KV tiles a run
-  long long n = 2 * (long long)num_sms() / items;
-  if (n > most) n = most;
-  return n > 1 ? (int)n : 1;
-}
-inline size_t span_tc_partial_bytes(int items, int nsplit, int r_v) {
-  return nsplit > 1 ? (size_t)items * nsplit * 256 * (r_v + 2) * 4 : 0;
+// Prompt form (tensor cores; no selection).  Work items are two row tiles of
+// 128 rows of one (sequence, KV head): the first `full` of them whole, the
+// other `tail` cut into ns runs of KV tiles each.
+struct TcPlan {
+  int full, tail, ns;
+};
+TcPlan tc_plan(int B, int Hkv, int G, int n_tot, int max_seq_len, int sink, int window);
+inline size_t tc_partial_bytes(const TcPlan& p, int r_v) {
+  return p.ns > 1 ? (size_t)p.tail * p.ns * 256 * (r_v + 2) * 4 : 0;
 }
 cudaError_t launch_span_tc_bf16(const SpanArgs& a, cudaStream_t st, bool pdl);
 cudaError_t launch_span_tc_e4m3(const SpanArgs& a, cudaStream_t st, bool pdl);

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
     for (; seg < item_end; ++seg, ++u0) {
       __syncwarp();
       request();
-      mbar_wait(bars + warp * NST + slot, phase, a.status);
+      mbar_poll(bars + warp * NST + slot, phase, a.status);
       const uint2 tag = tags[warp][slot];
       const uint32_t st = ring + slot * UB;
       if (++slot == NST) {

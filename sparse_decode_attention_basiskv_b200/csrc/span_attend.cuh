@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
       __syncwarp();  // every lane is done with the slot that is filled next
       request();
       if constexpr (BULK) {
-        mbar_wait(bars + warp * NST + slot, phase, a.status);
+        mbar_poll(bars + warp * NST + slot, phase, a.status);
       } else {
         cp_async_wait_group<NST - 1>();
         __syncwarp();

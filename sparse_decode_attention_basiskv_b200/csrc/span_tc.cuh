@@ -9,25 +9,32 @@
 // A work item is (sequence, KV head, two tiles of 128 rows).  A row is a query
 // token and a head of the group (token-major), so the group's heads share each
 // Key and latent that is loaded, and a tile spans only 128 / G tokens of the
-// band.  Per 128-token KV tile and row tile: S = Q K^T (tcgen05, both operands
-// in shared memory), P = exp2(S - m) (registers), O += P Z (A from tensor
-// memory).  2 * 128 * 128 * (d + r_v) multiply-adds and 2 * 128 * 128
-// exponentials a KV tile: at d 128, r_v 64 the tensor cores need about 1540
-// clocks and the 16 exponentials a clock 2048, so the exponentials bound it.
+// band.  KV comes in tiles of 128 tokens and is multiplied in steps of 64: per
+// step and row tile S = Q K^T (tcgen05, both operands in shared memory),
+// P = exp2(S - m) (registers), O += P Z (A from tensor memory).  Two row tiles
+// and 128 tokens take 2 * 128 * 128 * (d + r_v) multiply-adds and 2 * 128 * 128
+// exponentials: at d 128, r_v 64 the tensor cores need 2100 clocks (a 128 x 64
+// x 16 product takes 49, not 32) and the 16 exponentials a clock 2050.
 //
-// Roles (13 warps, one CTA an SM): warps 0-3 and 4-7 hold the softmax of one
-// row tile each, a thread a row (no shuffles).  The weights are taken against
-// the reference maximum at hand in one pass over S, which also finds the tile's
-// maximum; only where a row's has passed the reference by a wide margin does the
-// warp move it, rescale O and take the pass again.  Warps 8-11 bring in the KV
-// tiles page by page into the swizzled layout (bf16 by cp.async; E4M3 and
-// 4-bit rows widened to f16 on the way, exactly), a tile ahead of what they
-// hand over; warp 12 issues the MMAs, row tile 1's while row tile 0's softmax
-// runs and the other way round.  Tensor memory: S 2 x 128 columns (P over the
-// first 64 of each), O 2 x 128.
+// Roles (16 warps, one CTA an SM): warps 0 and 1 issue the MMAs of one row tile
+// each; warps 4-7 and 8-11 hold the softmax of one row tile each, a thread a
+// row (no shuffles): the step's 64 scores in registers, their maximum, the
+// weights.  The weights are taken against a reference that only moves where a
+// row's maximum has passed it by a wide margin; then the warp rescales O.
+// Warps 12-15 bring in the KV tiles page by page into the swizzled layout (bf16
+// by cp.async; E4M3 and 4-bit rows widened to f16 on the way, exactly), a tile
+// ahead of what they hand over.
 //
-// Few items: the KV tiles of an item are cut into nsplit runs, whose partial
-// sums span_tc_merge_kernel joins.
+// Tensor memory: per row tile two slots of 64 columns for S, P over the first
+// 32 of its S, and 128 for O.  Q K^T of step i + 2 follows P Z of step i on the
+// tensor cores into the same slot, while the softmax has step i + 1 before it,
+// so its latency is hidden.  (One slot of 128 columns a row tile, the softmax
+// waiting for each product, took 300 us where this takes 280, at a
+// 4096-token chunk of the Llama-8B layer over a window of 4096, bf16.)
+//
+// The items that would not fill a last round of the SMs (all of them, where
+// there are fewer items than SMs) have their KV tiles cut into runs, a block
+// each, whose partial sums span_tc_merge_kernel joins.
 #pragma once
 
 #include "cache4.cuh"
@@ -39,7 +46,7 @@
 namespace basiskv {
 namespace {
 
-constexpr int kTcThreads = 416;
+constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;  // two row tiles
 // How far (log2) scores may pass the reference before it moves: the weights then
 // reach 2^15 in f16, 2^64 in bf16, whose products and sums stay far inside
@@ -68,21 +75,24 @@ struct TcItem {
   int lo_first;         // first window token of the first row
   int n_sink, tile0, n; // KV tiles
 };
-__device__ __forceinline__ TcItem tc_item(const SpanArgs& a, int item) {
+__device__ __forceinline__ TcItem tc_place(const SpanArgs& a, int item) {
   TcItem x;
-  const int tq2 = kTcRows / a.G, njt = (a.n_tot + tq2 - 1) / tq2;
-  const int bg = item % (a.B * a.Hkv);
+  const int tq2 = kTcRows >> a.logG, njt = (a.n_tot + tq2 - 1) >> (8 - a.logG);
+  const int groups = a.B * a.Hkv, jt = item / groups, bg = item - jt * groups;
   // the last tiles of a chunk see the most tokens: they go first
-  x.j0 = (njt - 1 - item / (a.B * a.Hkv)) * tq2;
+  x.j0 = (njt - 1 - jt) * tq2;
   x.b = bg / a.Hkv;
   x.g = bg - x.b * a.Hkv;
-  int T = a.seq_lens[x.b];
+  return x;
+}
+__device__ __forceinline__ void tc_span(const SpanArgs& a, TcItem& x) {
+  int T = __ldg(a.seq_lens + x.b);
   if (T < 0 || T > a.max_seq_len) {
     if (threadIdx.x == 0) raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
     T = 0;
   }
   x.pos0 = T - a.n_tot + x.j0;
-  const int last = min(x.pos0 + tq2, T) - 1;
+  const int last = min(x.pos0 + (kTcRows >> a.logG), T) - 1;
   x.live_end = T > 0 ? last + 1 : 0;
   x.lo_first = a.window > 0 ? max(0, max(x.pos0, 0) - a.window + 1) : 0;
   if (x.live_end <= 0) {
@@ -92,7 +102,6 @@ __device__ __forceinline__ TcItem tc_item(const SpanArgs& a, int item) {
     x.n_sink = min((a.sink + 127) >> 7, x.tile0);
     x.n = x.n_sink + (last >> 7) - x.tile0 + 1;
   }
-  return x;
 }
 __device__ __forceinline__ int tc_tile(const TcItem& x, int i) {
   return i < x.n_sink ? i : x.tile0 + i - x.n_sink;
@@ -111,39 +120,79 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
                : "memory");
 }
 
+// Two fp32 lanes an instruction: a * b + c and a + b on register pairs.
+__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// One arrival for the whole warp, after all its lanes' work before it.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 template <int FMT, int D, int RV>
-__global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int nsplit) {
+__global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPlan plan) {
   using Gm = TcGeom<D, RV>;
   constexpr int NST = Gm::kStages;
   constexpr bool BF = FMT == kSpanBf16;
   extern __shared__ uint8_t tc_smem_raw[];
   uint8_t* smem = align_smem_1k(tc_smem_raw);
-  __shared__ uint64_t bars[4 * NST + 6];
+  __shared__ uint64_t bars[4 * NST + 13];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float row_scale[kTcRows];
   uint64_t *kfull = bars, *kempty = bars + NST, *zfull = bars + 2 * NST, *zempty = bars + 3 * NST;
-  uint64_t *sfull = bars + 4 * NST, *pfull = sfull + 2, *ofull = sfull + 4;
+  // [row tile][slot]: S is there, P is there, O has the step
+  uint64_t *sfull = bars + 4 * NST, *pfull = sfull + 4, *ofull = sfull + 8, *qfull = sfull + 12;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const uint32_t sq = smem_u32(smem), sk = sq + Gm::kQBytes, sz = sk + NST * Gm::kKBytes;
 
+  // the first plan.full blocks take whole items, the others one of plan.ns runs
+  const bool whole = (int)blockIdx.x < plan.full;
+  const int part = (int)blockIdx.x - plan.full;
+  TcItem it = tc_place(a, whole ? (int)blockIdx.x : plan.full + part / plan.ns);
+  const int split = whole ? 0 : part % plan.ns, nsplit = whole ? 1 : plan.ns;
+  const int rows = min(kTcRows, (a.n_tot - it.j0) << a.logG);  // live rows of the item
+  const int nt = rows > 128 ? 2 : 1;                           // row tiles
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&kfull[s], 128);
-      mbar_init(&zfull[s], 128);
-      mbar_init(&kempty[s], 1);
-      mbar_init(&zempty[s], 1);
+      mbar_init(&kfull[s], 4);  // one arrival a warp
+      mbar_init(&zfull[s], 4);
+      mbar_init(&kempty[s], nt);  // one commit a row tile
+      mbar_init(&zempty[s], nt);
     }
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 4; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[t], 128);
+      mbar_init(&pfull[t], 4);
       mbar_init(&ofull[t], 1);
     }
+    mbar_init(qfull, 8);
     abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tmem_slot)),
                  "r"(512)
@@ -153,122 +202,100 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
   pdl_wait();
   pdl_launch_dependents();
 
-  const TcItem it = tc_item(a, blockIdx.x / nsplit);
-  const int split = blockIdx.x % nsplit;
+  // the first batch of the item's queries, under the length's round trip
+  constexpr int QC = D / 8, QN = kTcRows * QC / 256, QB = QN < 8 ? QN : 8;
+  const uint16_t* q0 = a.q + ((size_t)it.b * a.n_tot + it.j0) * a.Hq * D + it.g * a.G * D;
+  auto load_q = [&](uint4 (&qv)[QB], int x0) {
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+      const int y = (x0 + x) * 256 + tid - 128, r = y / QC;
+      qv[x] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows)  // a token's heads of the group lie one behind the other
+        qv[x] = __ldg(reinterpret_cast<const uint4*>(
+            q0 + (size_t)(r >> a.logG) * a.Hq * D + (r & (a.G - 1)) * D + 8 * (y % QC)));
+    }
+  };
+  uint4 qv[QB];
+  if (warp >= 4 && warp < 12) load_q(qv, 0);
+  tc_span(a, it);
   const int i0 = (int)((long long)it.n * split / nsplit);
   const int n = (int)((long long)it.n * (split + 1) / nsplit) - i0;
-  const int tq = 128 / a.G;
-  const int rows = min(kTcRows, (a.n_tot - it.j0) * a.G);  // live rows of the item
-  const int nt = rows > 128 ? 2 : 1;                       // row tiles
-
-  // ---- queries into the swizzled layout, D / 8 lanes a row
-  {
-    constexpr int QC = D / 8;
-    for (int i = tid; i < kTcRows * QC; i += kTcThreads) {
-      const int r = i / QC, c = i - r * QC;
-      const int j = r / a.G, h = r - j * a.G;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows)
-        v = __ldg(reinterpret_cast<const uint4*>(
-            a.q + (((size_t)it.b * a.n_tot + it.j0 + j) * a.Hq + it.g * a.G + h) * D + 8 * c));
-      float scale = 1.f;
-      if constexpr (!BF) {
-        // f16 of the row times a power of two (largest magnitude in [2^14, 2^15))
-        uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        float m = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = bf16x2_to_f2(u[k]);
-          m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-#pragma unroll
-        for (int o = 1; o < QC; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int ex = m > 0.f ? (int)((__float_as_uint(m) >> 23) & 0xffu) - 126 : 15;
-        const int sh = max(-126, min(126, 15 - ex));
-        const float sc = __uint_as_float((uint32_t)(127 + sh) << 23);
-        scale = __uint_as_float((uint32_t)(127 - sh) << 23);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = bf16x2_to_f2(u[k]);
-          const __half2 hh = __floats2half2_rn(f.x * sc, f.y * sc);
-          u[k] = *reinterpret_cast<const uint32_t*>(&hh);
-        }
-        v = make_uint4(u[0], u[1], u[2], u[3]);
-      }
-      const int t = r >> 7;
-      sts128(sq + t * (Gm::kQBytes / 2) + tc_off(r & 127, c), v.x, v.y, v.z, v.w);
-      if (c == 0) row_scale[r] = scale;
-    }
-  }
-  fence_proxy_async();
+  const int tq = 128 >> a.logG;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int* abrt = &abort_flag;
+  // steps of 64 tokens; the last tile's second half may be past every row
+  const int n2 = n == 0 ? 0
+                        : 2 * n - (i0 + n == it.n && ((it.live_end - 1) & 127) < 64 ? 1 : 0);
 
-  if (warp == 12) {
-    // ------------------------------------------------------------ MMA issue
-    if (n > 0) {
-      constexpr uint32_t id_qk = tc_idesc(128, 128, BF, false);
+  if (warp < 2) {
+    // --------------------------------------- MMA issue, one warp a row tile
+    const int t = warp;
+    if (n > 0 && t < nt) {
+      constexpr uint32_t id_qk = tc_idesc(128, 64, BF, false);
       constexpr uint32_t id_pv = tc_idesc(128, RV, BF, true);
-      const uint64_t dq = tc_sdesc(sq), dk = tc_sdesc(sk), dz = tc_sdesc(sz, 16384);
+      const uint64_t dq = tc_sdesc(sq + t * (Gm::kQBytes / 2)), dk = tc_sdesc(sk),
+                     dz = tc_sdesc(sz, 16384);
+      const uint32_t tm_s = tmem + 128 * t, tm_o = tmem + 256 + 128 * t;
       const bool lead = elect_one();
-      auto qk = [&](int t, int stage) {
-        const uint64_t q = dq + t * (Gm::kQBytes / 2 >> 4), k0 = dk + stage * (Gm::kKBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma_ss(tmem + 128 * t, q + (k >> 2) * 1024 + (k & 3) * 2,
-                    k0 + (k >> 2) * 1024 + (k & 3) * 2, id_qk, k > 0);
-        tc_commit_to(&sfull[t]);
+      auto wait = [&](uint64_t* bar, int parity) {
+        return mbar_poll(bar, parity, a.status, abrt);
       };
-      auto pv = [&](int t, int stage, bool first) {
-        const uint64_t z = dz + stage * (Gm::kZBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, z + k * 128, id_pv,
-                    !first || k > 0);
-        tc_commit_to(&ofull[t]);
-      };
-      bool ok = mbar_wait_or_abort(&kfull[0], 0, a.status, abrt);
-      if (ok) {
+      // step u of KV tile u / 2 in ring stage st: rows 64 (u % 2) .. of the tile
+      auto qk = [&](int u, int st) {
         tc_fence_after_sync();
         if (lead) {
-          qk(0, 0);
-          if (nt == 2) qk(1, 0);
-          tc_commit_to(&kempty[0]);
+          const uint64_t k0 = dk + st * (Gm::kKBytes >> 4) + (u & 1) * (64 * 128 >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_ss(tm_s + 64 * (u & 1), dq + (k >> 2) * 1024 + (k & 3) * 2,
+                      k0 + (k >> 2) * 1024 + (k & 3) * 2, id_qk, k > 0);
+          tc_commit_to(&sfull[2 * t + (u & 1)]);
+          if (u & 1) tc_commit_to(&kempty[st]);
         }
+        __syncwarp();
+      };
+      int kst = 0, kph = 0, zst = 0, zph = 0;  // stages of the next Key and latent tiles
+      auto next = [](int& st, int& ph) {
+        if (++st == NST) {
+          st = 0;
+          ph ^= 1;
+        }
+      };
+      bool ok = wait(qfull, 0) && wait(&kfull[0], 0);
+      if (ok) {
+        qk(0, 0);
+        if (n2 > 1) qk(1, 0);
+        next(kst, kph);
       }
-      int st = 0, st_ph = 0;  // ring stage of tile i and its turn
-      for (int i = 0; ok && i < n; ++i) {
-        const int nx = st + 1 == NST ? 0 : st + 1, nx_ph = st_ph ^ (nx == 0);
-        for (int t = 0; ok && t < nt; ++t) {
-          if (t == 0) {
-            ok = mbar_wait_or_abort(&zfull[st], st_ph, a.status, abrt);
-            if (ok && i + 1 < n) ok = mbar_wait_or_abort(&kfull[nx], nx_ph, a.status, abrt);
-          }
-          if (ok) ok = mbar_wait_or_abort(&pfull[t], i & 1, a.status, abrt);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          if (lead) {
-            pv(t, st, i == 0);
-            if (t == nt - 1) tc_commit_to(&zempty[st]);
-            if (i + 1 < n) {
-              qk(t, nx);
-              if (t == nt - 1) tc_commit_to(&kempty[nx]);
-            }
-          }
+      for (int u = 0; ok && u < n2; ++u) {
+        if (!(u & 1)) ok = wait(&zfull[zst], zph);
+        ok = ok && wait(&pfull[2 * t + (u & 1)], (u >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (lead) {
+          const uint64_t z = dz + zst * (Gm::kZBytes >> 4) + (u & 1) * (64 * 128 >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + k * 128, id_pv, u > 0 || k > 0);
+          tc_commit_to(&ofull[2 * t + (u & 1)]);
+          if (u & 1) tc_commit_to(&zempty[zst]);
         }
-        st = nx;
-        st_ph = nx_ph;
+        __syncwarp();
+        if (u & 1) next(zst, zph);
+        if (u + 2 < n2) {
+          if (!(u & 1)) ok = wait(&kfull[kst], kph);
+          if (!ok) break;
+          qk(u, kst);  // step u + 2: the next tile's half of the same parity
+          if (u & 1) next(kst, kph);
+        }
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // -------------------------------------------------------------- loaders
-    const int lt = tid - 256;  // 0 .. 127
+    const int lt = tid - 384;  // 0 .. 127
     // tokens some row of the item sees; the rest of a tile is zeroed
     auto seen = [&](int t) { return t < it.live_end && (t >= it.lo_first || t < a.sink); };
     // The tile row of token t, -1 when there is nothing to read.
@@ -288,26 +315,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
       const int w = lt >> 5;
       constexpr int KC = D / 8, ZC = RV / 8;
       auto copy_k = [&](int i, int row) {
-        const uint32_t dst = sk + (i % NST) * Gm::kKBytes;
-#pragma unroll
+        const uint32_t dst = sk + (i % NST) * Gm::kKBytes + 32 * w * 128;
+        const uint8_t* src = a.K + (lane % KC) * 16;
+#pragma unroll 4
         for (int x = 0; x < KC; ++x) {
-          const int y = 32 * x + lane, r = y / KC, c = y % KC;
+          const int r = (32 * x + lane) / KC, c = lane % KC;
           const int tr = __shfl_sync(0xffffffffu, row, r);
-          cp_async16_or_zero(dst + tc_off(32 * w + r, c),
-                             a.K + (tr < 0 ? 0 : ((size_t)tr * D + 8 * c) * 2), tr >= 0);
+          cp_async16_or_zero(dst + tc_off(r, c), src + (tr < 0 ? 0 : (int64_t)tr * (D * 2)),
+                             tr >= 0);
         }
       };
       auto copy_z = [&](int i, int row) {
-        const uint32_t dst = sz + (i % NST) * Gm::kZBytes;
-#pragma unroll
-        for (int x = 0; x < ZC; ++x) {
-          const int y = 32 * x + lane, r = y / ZC, c = y % ZC;
-          const int tr = __shfl_sync(0xffffffffu, row, r);
-          size_t off = 0;
-          if (tr >= 0)
-            off = ((size_t)(tr >> a.logS) * a.S * RV +
-                   split_off(tr & (a.S - 1), 8 * c, a.S, RV, a.zsplit)) * 2;
-          cp_async16_or_zero(dst + tc_off(32 * w + r, c), a.Z + off, tr >= 0);
+        const uint32_t dst = sz + (i % NST) * Gm::kZBytes + 32 * w * 128;
+        if (a.zsplit == RV) {
+#pragma unroll 4
+          for (int x = 0; x < ZC; ++x) {
+            const int y = 32 * x + lane, r = y / ZC, c = y % ZC;
+            const int tr = __shfl_sync(0xffffffffu, row, r);
+            cp_async16_or_zero(dst + tc_off(r, c),
+                               a.Z + c * 16 + (tr < 0 ? 0 : (int64_t)tr * (RV * 2)), tr >= 0);
+          }
+        } else {  // a narrow router's split tiles
+#pragma unroll 1
+          for (int x = 0; x < ZC; ++x) {
+            const int y = 32 * x + lane, r = y / ZC, c = y % ZC;
+            const int tr = __shfl_sync(0xffffffffu, row, r);
+            size_t off = 0;
+            if (tr >= 0)
+              off = ((size_t)(tr >> a.logS) * a.S * RV +
+                     split_off(tr & (a.S - 1), 8 * c, a.S, RV, a.zsplit)) * 2;
+            cp_async16_or_zero(dst + tc_off(r, c), a.Z + off, tr >= 0);
+          }
         }
       };
       // groups in flight: K_0, Z_0, K_1, Z_1, ...; a part is handed over when
@@ -316,31 +354,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
       bool ok = true;
       for (int i = 0; i < n; ++i) {
         const int next = i + 1 < n ? tile_row(tc_tile(it, i0 + i + 1) * 128 + lt) : -1;
-        if (i >= NST) ok = mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (i >= NST) ok = mbar_poll(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!ok) break;
         copy_k(i, row);
         cp_async_commit();
-        if (i > 0) {
+        if (i > 1) {
           cp_async_wait_group<2>();
           fence_proxy_async();
-          mbar_arrive(&kfull[(i - 1) % NST]);
+          arrive_warp(&kfull[(i - 1) % NST]);
         }
-        if (i >= NST) ok = mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (i >= NST) ok = mbar_poll(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!ok) break;
         copy_z(i, row);
         cp_async_commit();
+        if (i == 0) {  // nothing is under way yet: the first Keys at once
+          cp_async_wait_group<1>();
+          fence_proxy_async();
+          arrive_warp(&kfull[0]);
+        }
         if (i > 0) {
           cp_async_wait_group<2>();
           fence_proxy_async();
-          mbar_arrive(&zfull[(i - 1) % NST]);
+          arrive_warp(&zfull[(i - 1) % NST]);
         }
         row = next;
       }
       cp_async_wait_all();
       fence_proxy_async();
       if (n > 0 && ok) {
-        mbar_arrive(&kfull[(n - 1) % NST]);
-        mbar_arrive(&zfull[(n - 1) % NST]);
+        if (n > 1) arrive_warp(&kfull[(n - 1) % NST]);
+        arrive_warp(&zfull[(n - 1) % NST]);
       }
     } else {
       // A thread widens one row of each tile; the next tile's bytes are
@@ -413,16 +456,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
       };
       bool ok = true;
       auto hand_over = [&](const Raw& x, int i) {
-        if (i >= NST) ok = mbar_wait_or_abort(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (i >= NST) ok = mbar_poll(&kempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!ok) return false;
         put(sk + (i % NST) * Gm::kKBytes, x.row >= 0, x.kw, D, x.ks);
         fence_proxy_async();
-        mbar_arrive(&kfull[i % NST]);
-        if (i >= NST) ok = mbar_wait_or_abort(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        arrive_warp(&kfull[i % NST]);
+        if (i >= NST) ok = mbar_poll(&zempty[i % NST], ((i / NST) & 1) ^ 1, a.status, abrt);
+        if (!ok) return false;
         put(sz + (i % NST) * Gm::kZBytes, x.row >= 0, x.zw, RV, x.zs);
         fence_proxy_async();
-        mbar_arrive(&zfull[i % NST]);
+        arrive_warp(&zfull[i % NST]);
         return true;
       };
       Raw x0, x1;
@@ -437,132 +480,147 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
         if (!hand_over(x1, i + 1)) break;
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // -------------------------------------------------------------- softmax
-    const int t = warp >> 2, r = tid & 127, row = t * 128 + r;
+    // queries into the swizzled layout first, D / 8 lanes a row
+    {
+#pragma unroll
+      for (int x0 = 0; x0 < QN; x0 += QB) {
+        if (x0 > 0) load_q(qv, x0);
+#pragma unroll
+        for (int x = 0; x < QB; ++x) {
+          const int y = (x0 + x) * 256 + tid - 128, r = y / QC, c = y % QC;
+          uint32_t u[4] = {qv[x].x, qv[x].y, qv[x].z, qv[x].w};
+          if constexpr (!BF) {
+            // f16 of the row times a power of two (largest magnitude in [2^14, 2^15))
+            float mq = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = bf16x2_to_f2(u[k]);
+              mq = fmaxf(mq, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+#pragma unroll
+            for (int o = 1; o < QC; o <<= 1) mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, o));
+            const int ex = mq > 0.f ? (int)((__float_as_uint(mq) >> 23) & 0xffu) - 126 : 15;
+            const int sh = max(-126, min(126, 15 - ex));
+            const float sc = __uint_as_float((uint32_t)(127 + sh) << 23);
+            if (c == 0) row_scale[r] = __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = bf16x2_to_f2(u[k]);
+              const __half2 hh = __floats2half2_rn(f.x * sc, f.y * sc);
+              u[k] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+          }
+          sts128(sq + (r >> 7) * (Gm::kQBytes / 2) + tc_off(r & 127, c), u[0], u[1], u[2], u[3]);
+        }
+      }
+      fence_proxy_async();
+      arrive_warp(qfull);
+      if (!BF) named_bar_sync(1, 256);  // row_scale
+    }
+    const int t = (warp >> 2) - 1, r = tid & 127, row = t * 128 + r;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
     if (t < nt) {
-      const int j = row / a.G, h = row - j * a.G;
+      const int j = row >> a.logG, h = row & (a.G - 1);
       const bool live = row < rows;
       const int pos = live ? it.pos0 + j : -1;
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       // the row tile's first and last positions
       const int pos_a = it.pos0 + t * tq, pos_b = min(it.pos0 + (t + 1) * tq, it.live_end) - 1;
       const int lo_b = a.window > 0 ? max(0, pos_b - a.window + 1) : 0;
-      const float sl = a.scale_log2 * row_scale[row];
+      const float sl = BF ? a.scale_log2 : a.scale_log2 * row_scale[row];
+      const uint64_t sl2 = pack2(__float_as_uint(sl), __float_as_uint(sl));
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int i = 0; i < n; ++i) {
-        ok = mbar_wait_or_abort(&sfull[t], i & 1, a.status, abrt);
+      for (int u = 0; u < n2; ++u) {
+        const uint32_t tu = ts + 64 * (u & 1);
+        ok = mbar_poll(&sfull[2 * t + (u & 1)], (u >> 1) & 1, a.status, abrt);
+        // No phase of `ofull` is skipped, so a wait's parity names one phase (step
+        // u - 2 is multiplied by now, but its arrival may be seen after S's).
+        if (u > 1) ok = mbar_poll(&ofull[2 * t + (u & 1)], ((u >> 1) - 1) & 1, a.status, abrt) && ok;
         if (!ok) break;
         tc_fence_after_sync();
-        const int t0 = tc_tile(it, i0 + i) * 128;
-        const bool masked = !(t0 + 127 <= pos_a && (t0 >= lo_b || t0 + 127 < a.sink));
-        uint32_t sa[16], sb[16], p[64];
-        if (masked) {
+        uint32_t sa[32], sb[32], p[32];
+        tc_ld32(tu, sa);
+        tc_ld32(tu + 32, sb);
+        const int t0 = tc_tile(it, i0 + (u >> 1)) * 128 + 64 * (u & 1);
+        tc_wait_ld(sa);
+        tc_wait_ld(sb);
+        if (!(t0 + 63 <= pos_a && (t0 >= lo_b || t0 + 63 < a.sink))) {
           // column x holds token t0 + x: visible up to pos, from lo on or below
-          // the sinks' end; the others become -inf in place
+          // the sinks' end
           const int me = pos - t0, mf = lo - t0, mg = a.sink - t0;
-#pragma unroll 1
-          for (int x0 = 0; x0 < 128; x0 += 32) {
-            tc_ld32(ts + x0, p);
-            tc_wait_ld(p);
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (x0 + x > me || (x0 + x < mf && x0 + x >= mg)) p[x] = 0xff800000u;
-            tc_st32(ts + x0, p);
+          for (int x = 0; x < 32; ++x) {
+            if (x > me || (x < mf && x >= mg)) sa[x] = 0xff800000u;
+            if (x + 32 > me || (x + 32 < mf && x + 32 >= mg)) sb[x] = 0xff800000u;
           }
-          tc_wait_st();
         }
-        auto max16 = [&](const uint32_t (&s)[16], float v) {
+        float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < 16; x += 2)
-            v = fmaxf(v, fmaxf(__uint_as_float(s[x]), __uint_as_float(s[x + 1])));
-          return v;
-        };
-        if (i == 0) {  // the first tile sets the reference
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int x = 0; x < 128; x += 16) {
-            tc_ld16(ts + x, sa);
-            tc_wait_ld16(sa);
-            mx = max16(sa, mx);
-          }
-          m = mx * sl;
+        for (int x = 0; x < 32; x += 2) {
+          mx = max3(mx, __uint_as_float(sa[x]), __uint_as_float(sa[x + 1]));
+          my = max3(my, __uint_as_float(sb[x]), __uint_as_float(sb[x + 1]));
         }
-        float sum0, sum1;
-        for (;;) {
-          const float base = m == -INFINITY ? 0.f : m;
-          float mx = -INFINITY;
-          sum0 = sum1 = 0.f;
-          // (scalar products: the packed two-lane forms measured slower here)
-          auto weights = [&](uint32_t (&s)[16], int x) {
-            mx = max16(s, mx);
-#pragma unroll
-            for (int y = 0; y < 16; y += 2) {
-              const float p0 = ex2(fmaf(__uint_as_float(s[y]), sl, -base));
-              const float p1 = ex2(fmaf(__uint_as_float(s[y + 1]), sl, -base));
-              sum0 += p0;
-              sum1 += p1;
-              if constexpr (BF) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
-                p[(x + y) / 2] = *reinterpret_cast<const uint32_t*>(&v);
-              } else {
-                const __half2 v = __floats2half2_rn(p0, p1);
-                p[(x + y) / 2] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-            }
-            // done with these scores before the next ones come
-            asm volatile("" : "+f"(mx), "+f"(sum0), "+f"(sum1));
-          };
-          tc_ld16(ts, sa);
-          tc_wait_ld16(sa);
-#pragma unroll
-          for (int x = 0; x < 128; x += 32) {
-            tc_ld16(ts + x + 16, sb);
-            weights(sa, x);
-            tc_wait_ld16(sb);
-            if (x + 32 < 128) tc_ld16(ts + x + 32, sa);
-            weights(sb, x + 16);
-            if (x + 32 < 128) tc_wait_ld16(sa);
-          }
-          mx *= sl;
-          const bool grow = mx > m + tc_slack<FMT>();
-          if (!__any_sync(0xffffffffu, grow)) break;
-          // (not at i = 0, where the reference is the maximum)
+        mx = fmaxf(mx, my) * sl;
+        const bool grow = u == 0 || mx > m + tc_slack<FMT>();
+        if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2(m - mx) : 1.f;
           if (grow) m = mx;
-          l *= f;
-          ok = i > 0 ? mbar_wait_or_abort(&ofull[t], (i - 1) & 1, a.status, abrt) : ok;
-          if (!__all_sync(0xffffffffu, ok)) break;
-          tc_fence_after_sync();
+          if (u > 0) {  // O is complete up to the step before this one
+            l *= f;
+            ok = mbar_poll(&ofull[2 * t + ((u - 1) & 1)], ((u - 1) >> 1) & 1, a.status, abrt);
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int x = 0; x < RV; x += 32) {
+              tc_ld32(to + x, p);
+              tc_wait_ld(p);
 #pragma unroll
-          for (int x = 0; x < RV / 32; ++x) {  // p is free here: the pass is taken again
-            tc_ld32(to + 32 * x, p);
-            tc_wait_ld(p);
-#pragma unroll
-            for (int y = 0; y < 32; ++y) p[y] = __float_as_uint(__uint_as_float(p[y]) * f);
-            tc_st32(to + 32 * x, p);
+              for (int y = 0; y < 32; ++y) p[y] = __float_as_uint(__uint_as_float(p[y]) * f);
+              tc_st32(to + x, p);
+            }
           }
         }
-        if (!__all_sync(0xffffffffu, ok)) break;
-        // P over the first 64 columns of S, which every lane has read
-        tc_st32(ts, p);
-        tc_st32(ts + 32, p + 32);
+        const uint32_t nb = __float_as_uint(m == -INFINITY ? 0.f : -m);
+        const uint64_t nbase = pack2(nb, nb);
+        uint64_t sum = 0;
+        auto weights = [&](const uint32_t (&s)[32], uint32_t* out) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            float p0, p1;
+            unpack2(fma2(pack2(s[y], s[y + 1]), sl2, nbase), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum = add2(sum, pack2(__float_as_uint(p0), __float_as_uint(p1)));
+            if constexpr (BF) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+              out[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
+            } else {
+              const __half2 v = __floats2half2_rn(p0, p1);
+              out[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          }
+        };
+        weights(sa, p);
+        weights(sb, p + 16);
+        tc_st32(tu, p);  // over the first 32 columns of S
+        float sum0, sum1;
+        unpack2(sum, sum0, sum1);
         l += sum0 + sum1;
         tc_wait_st();
         tc_fence_before_sync();
-        mbar_arrive(&pfull[t]);
+        arrive_warp(&pfull[2 * t + (u & 1)]);
       }
-      if (n > 0 && __all_sync(0xffffffffu, ok))
-        ok = mbar_wait_or_abort(&ofull[t], (n - 1) & 1, a.status, abrt);
-      if (__all_sync(0xffffffffu, ok)) {
+      if (n > 0 && ok) ok = mbar_poll(&ofull[2 * t + ((n2 - 1) & 1)], ((n2 - 1) >> 1) & 1, a.status, abrt);
+      if (ok) {
         tc_fence_after_sync();
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const size_t slot = blockIdx.x;
+        const size_t slot = part;
         float* po = a.partial + (slot * kTcRows + row) * RV;
-        float* pm = a.partial + ((size_t)gridDim.x * kTcRows * RV) + (slot * kTcRows + row) * 2;
+        float* pm = a.partial + (size_t)plan.tail * plan.ns * kTcRows * RV + (slot * kTcRows + row) * 2;
         uint16_t* out =
             a.out + (((size_t)it.b * a.n_tot + it.j0 + j) * a.Hq + it.g * a.G + h) * RV;
 #pragma unroll
@@ -605,19 +663,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, int 
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 12)
+  if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
 }
 
-// Joins the nsplit partial sums of every row: a thread 4 columns.
+// Joins the plan.ns partial sums of every row of the split items: a thread 4
+// columns.
 template <int RV>
-__global__ void __launch_bounds__(256) span_tc_merge_kernel(SpanArgs a, int nsplit, int items) {
+__global__ void __launch_bounds__(256) span_tc_merge_kernel(SpanArgs a, TcPlan plan) {
   pdl_wait();
   pdl_launch_dependents();
-  const TcItem it = tc_item(a, blockIdx.x);
-  const int rows = min(kTcRows, (a.n_tot - it.j0) * a.G);
-  const float* ml = a.partial + (size_t)items * nsplit * kTcRows * RV;
+  const TcItem it = tc_place(a, plan.full + blockIdx.x);
+  const int rows = min(kTcRows, (a.n_tot - it.j0) << a.logG), nsplit = plan.ns;
+  const float* ml = a.partial + (size_t)plan.tail * nsplit * kTcRows * RV;
   for (int o = blockIdx.y * 256 + threadIdx.x; o < rows * (RV / 4); o += gridDim.y * 256) {
     const int row = o / (RV / 4), c = (o - row * (RV / 4)) * 4;
     float M = -INFINITY, L = 0.f;
@@ -638,7 +697,7 @@ __global__ void __launch_bounds__(256) span_tc_merge_kernel(SpanArgs a, int nspl
       M = mn;
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    const int j = row / a.G, h = row - j * a.G;
+    const int j = row >> a.logG, h = row & (a.G - 1);
     const __nv_bfloat162 u = __floats2bfloat162_rn(A.x * inv, A.y * inv);
     const __nv_bfloat162 w = __floats2bfloat162_rn(A.z * inv, A.w * inv);
     *reinterpret_cast<uint2*>(
@@ -649,18 +708,17 @@ __global__ void __launch_bounds__(256) span_tc_merge_kernel(SpanArgs a, int nspl
 
 template <int FMT, int D, int RV>
 cudaError_t launch_span_tc_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
-  const int items = span_tc_items(a.B, a.Hkv, a.G, a.n_tot);
-  const int nsplit = span_tc_splits(items, a.n_tot, a.max_seq_len, a.sink, a.window);
+  const TcPlan plan = tc_plan(a.B, a.Hkv, a.G, a.n_tot, a.max_seq_len, a.sink, a.window);
   cudaError_t e = cudaFuncSetAttribute(span_tc_kernel<FMT, D, RV>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)TcGeom<D, RV>::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_k(span_tc_kernel<FMT, D, RV>, dim3(items * nsplit), dim3(kTcThreads),
-               TcGeom<D, RV>::kSmem, st, pdl, a, nsplit);
-  if (e != cudaSuccess || nsplit == 1) return e;
+  e = launch_k(span_tc_kernel<FMT, D, RV>, dim3(plan.full + plan.tail * plan.ns),
+               dim3(kTcThreads), TcGeom<D, RV>::kSmem, st, pdl, a, plan);
+  if (e != cudaSuccess || plan.ns == 1) return e;
   const int rows = a.n_tot * a.G < kTcRows ? a.n_tot * a.G : kTcRows;
-  return launch_k(span_tc_merge_kernel<RV>, dim3(items, (rows * (RV / 4) + 255) / 256), dim3(256),
-                  0, st, pdl, a, nsplit, items);
+  return launch_k(span_tc_merge_kernel<RV>, dim3(plan.tail, (rows * (RV / 4) + 255) / 256),
+                  dim3(256), 0, st, pdl, a, plan);
 }
 
 template <int FMT>
