@@ -115,26 +115,13 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
   return true;
 }
 
-// The waits for barriers that a kernel meets every microsecond: they look at the
-// clock and the flag at every 256th poll only.  mbar_poll suspends the thread
-// between polls (mbarrier.try_wait), which frees issue slots but was measured to
-// notice an arrival up to 1000 clocks late; mbar_spin does not.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; "
-      "selp.u32 %0, 1, 0, p; }"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-template <bool SPIN>
-__device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, unsigned int* status,
+// The wait for barriers that a kernel meets every microsecond: it looks at the
+// clock and the flag at every 256th poll only.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, unsigned int* status,
                                           volatile int* abort = nullptr) {
   unsigned int polls = 0;
   unsigned long long t0 = 0;
-  while (!(SPIN ? mbar_test(bar, parity) : mbar_try_wait(bar, parity))) {
+  while (!mbar_try_wait(bar, parity)) {
     if ((++polls & 0xffu) != 0) continue;
     if (abort && *abort) return false;
     const unsigned long long t = global_ns();
@@ -146,14 +133,6 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, un
     }
   }
   return true;
-}
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, unsigned int* status,
-                                          volatile int* abort = nullptr) {
-  return mbar_wait_for<false>(bar, parity, status, abort);
-}
-__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, unsigned int* status,
-                                          volatile int* abort = nullptr) {
-  return mbar_wait_for<true>(bar, parity, status, abort);
 }
 
 // ------------------------------------------------------------ TMA and bulk

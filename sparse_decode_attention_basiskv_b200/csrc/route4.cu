@@ -11,13 +11,20 @@
 // The units (32 tokens: one page of 32 or two of 16) of all (sequence, KV
 // head) items form one line, cut into equal contiguous runs, one a warp (a
 // scan of the lengths finds them, so ragged batches load every SM alike).  A
-// warp brings its units into its own ring, kR4Stages - 1 ahead: a tile is one
-// contiguous piece that one lane hands to the copy engine.  Tokens are the
+// warp brings its units into its own ring: a tile is one contiguous piece for the
+// copy engine, and the lanes that looked up the next units hand over half a ring
+// of them at a time, side by side.  Tokens are the
 // rows of mma.m16n8k16's A operand, as stored; B holds four heads, the f16
 // roundings of their folded queries in the even columns and the remainders in
 // the odd ones, so a lane's two sums give one fp32-accurate score (22
 // significant bits; each head is first scaled by a power of two that puts its
 // largest magnitude into [2^14, 2^15), divided out of the scores again).
+//
+// Measured: 16 x 32K tokens, 8 KV heads, r_v 64, r_k 32 (228 MB): 63 us with the
+// folding of the queries and the choice of pages, 3.6 TB/s; the instructions of the widening
+// bound it (about 13 a 32-token unit and column pair of a lane).  A ring a
+// warp with one unit requested at a time took 70 us, a fourth of the warps as
+// loaders for the others 101 us, two CTAs an SM instead of three 64 us.
 #include "cache4.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -30,12 +37,18 @@ namespace {
 constexpr int kR4Threads = kLineMaxSeqs;  // a thread scans a sequence's length
 constexpr int kR4Warps = kR4Threads / 32;
 constexpr int kR4Unit = 32;
-constexpr int kR4CtasPerSm = 2;
+// CTAs an SM: three where the registers (one group of heads, at most 96 columns)
+// and the ring allow.
+template <int W, int NJ>
+constexpr int r4_ctas() {
+  return NJ == 1 && W <= 96 ? 3 : 2;
+}
 
-// Ring depth: 4 units, 3 where shared memory ends.
-template <int W>
+// Ring depth: 8 units where shared memory holds them, else 4.
+template <int W, int NJ>
 constexpr int r4_stages() {
-  return 4 * kR4Warps * 18 * W <= 104 * 1024 ? 4 : 3;
+  const int n = (226 / r4_ctas<W, NJ>() - 5) * 1024 / (kR4Warps * 18 * W);
+  return n >= 8 ? 8 : (n >= 4 ? 4 : 2);
 }
 
 // The warp's maximum.
@@ -102,8 +115,9 @@ __device__ __forceinline__ void r4_part(uint32_t codes, uint32_t sc, int n, int 
 
 // NJ: groups of four heads (1 for G <= 4, 2 for G = 8).  ONE: pages of 32.
 template <int RV, int RK, int NJ, bool ONE>
-__global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4Args a) {
-  constexpr int W = RV + RK, KS = W / 16, UB = 18 * W, NST = r4_stages<W>();
+__global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
+    route4_kernel(Route4Args a) {
+  constexpr int W = RV + RK, KS = W / 16, UB = 18 * W, NST = r4_stages<W, NJ>(), NB = NST / 2;
   constexpr int PP = ONE ? 1 : 2;  // pages a unit
   extern __shared__ __align__(128) uint8_t r4_smem[];
   __shared__ long long pre[257];
@@ -141,9 +155,9 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
     const long long x = start + base + lane;
     const int b = line_find(a.B, pre, a.Hkv, x);
     const int U = (int)(pre[b + 1] - pre[b]);
-    const long long y = x - pre[b] * a.Hkv;
-    id_g = (int)(y / U);
-    const int p = (int)(y - (long long)id_g * U) * PP;
+    const unsigned y = (unsigned)(x - pre[b] * a.Hkv);  // below Hkv * U
+    id_g = (int)(y / (unsigned)U);
+    const int p = (int)(y - (unsigned)id_g * U) * PP;
     const int P = (a.seq_lens[b] + a.S - 1) / a.S;
     auto look = [&](int q) {
       int id = q < P ? __ldg(a.block_table + (size_t)b * a.max_pages + q) : -1;
@@ -156,10 +170,13 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
     id_a = look(p);
     if (PP == 2) id_b = look(p + 1);
   };
+  // Requests units k .. k + NB - 1 into slots `slot` ..: a lane each.
   auto issue = [&](int k, int slot) {
     if (k >= run) return;
     if (k - id_base >= 32) fetch_ids(k);
-    if (lane != k - id_base) return;
+    const int i = lane - (k - id_base);
+    if (i < 0 || i >= NB || k + i >= run) return;
+    slot += i;
     const uint32_t st = ring + slot * UB, b = bar + 8 * slot;
     auto copy = [&](uint32_t dst, const uint8_t* src, uint32_t bytes) {
       asm volatile(
@@ -167,18 +184,9 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
           "[%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(b)
           : "memory");
     };
-    const int present = (id_a >= 0) + (id_b >= 0);
-    tags[warp][slot] = make_uint2(id_a >= 0, id_b >= 0);
-    if (!present) {
-      asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(b)
-                   : "memory");
-      return;
-    }
     constexpr int TZ = (ONE ? 18 : 9) * RV, TE = (ONE ? 18 : 9) * RK;  // tile bytes
-    asm volatile(
-        "{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(b),
-        "r"(present * (TZ + TE))
-        : "memory");
+    tags[warp][slot] = make_uint2(id_a >= 0, id_b >= 0);
+    mbar_arrive_expect_tx(bars + warp * NST + slot, ((id_a >= 0) + (id_b >= 0)) * (TZ + TE));
     if (id_a >= 0) {
       const size_t t = (size_t)id_a * a.Hkv + id_g;
       copy(st, a.Z + t * TZ, TZ);
@@ -190,14 +198,10 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
       copy(st + 18 * RV + 9 * RK, a.E + t * TE, TE);
     }
   };
-  int k_next = 0, slot_next = 0;
-  auto request = [&]() {
-    issue(k_next++, slot_next);
-    slot_next = slot_next + 1 == NST ? 0 : slot_next + 1;
-  };
   if (run > 0) fetch_ids(0);
-#pragma unroll
-  for (int i = 0; i < NST - 1; ++i) request();
+  issue(0, 0);
+  issue(NB, NB);
+  int k_next = 2 * NB;
   int slot = 0;
   uint32_t phase = 0;
 
@@ -207,9 +211,9 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
       const long long x = start + seg;
       b = line_find(a.B, pre, a.Hkv, x);
       const int U = (int)(pre[b + 1] - pre[b]);
-      const long long y = x - pre[b] * a.Hkv;
-      g = (int)(y / U);
-      u0 = (int)(y - (long long)g * U);
+      const unsigned y = (unsigned)(x - pre[b] * a.Hkv);  // below Hkv * U
+      g = (int)(y / (unsigned)U);
+      u0 = (int)(y - (unsigned)g * U);
       item_end = min(run, seg + U - u0);
     }
     const int T = a.seq_lens[b];
@@ -250,15 +254,9 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
         }
     }
     for (; seg < item_end; ++seg, ++u0) {
-      __syncwarp();
-      request();
       mbar_poll(bars + warp * NST + slot, phase, a.status);
       const uint2 tag = tags[warp][slot];
       const uint32_t st = ring + slot * UB;
-      if (++slot == NST) {
-        slot = 0;
-        phase ^= 1;
-      }
       const int t0 = u0 * kR4Unit;
       float best[2];
 #pragma unroll
@@ -292,18 +290,28 @@ __global__ void __launch_bounds__(kR4Threads, kR4CtasPerSm) route4_kernel(Route4
         if (lane < 2 && (lane == 0 || t0 + 16 < T))
           out[2 * u0 + lane] = (lane ? tag.y : tag.x) ? (lane ? r1 : r0) : -INFINITY;
       }
+      ++slot;
+      if (slot == NB || slot == NST) {  // half the ring has been read by every lane
+        __syncwarp();
+        issue(k_next, slot - NB);
+        k_next += NB;
+        if (slot == NST) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
     }
   }
 }
 
 template <int RV, int RK, int NJ, bool ONE>
 cudaError_t launch_route4_t(const Route4Args& a, cudaStream_t st, bool pdl) {
-  constexpr size_t smem = (size_t)kR4Warps * r4_stages<RV + RK>() * 18 * (RV + RK);
+  constexpr size_t smem = (size_t)kR4Warps * r4_stages<RV + RK, NJ>() * 18 * (RV + RK);
   cudaError_t e = cudaFuncSetAttribute(route4_kernel<RV, RK, NJ, ONE>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const long long units = (long long)((a.max_seq_len + kR4Unit - 1) / kR4Unit) * a.B * a.Hkv;
-  long long grid = (long long)num_sms() * kR4CtasPerSm;
+  long long grid = (long long)num_sms() * r4_ctas<RV + RK, NJ>();
   if (grid > units / kR4Warps) grid = units / kR4Warps > 0 ? units / kR4Warps : 1;
   return launch_k(route4_kernel<RV, RK, NJ, ONE>, dim3((unsigned)grid), dim3(kR4Threads), smem,
                   st, pdl, a);
