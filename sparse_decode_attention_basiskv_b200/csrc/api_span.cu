@@ -99,7 +99,7 @@ SpanArgs span_args(const basiskv_dims* d, const basiskv_bf16* q, const int32_t* 
 }
 
 size_t span_partial_bytes(const basiskv_dims* d, int rows) {
-  return (span_slots(d->B, d->Hkv) * rows * (d->r_v + 2) * 4 + 255) & ~size_t(255);
+  return (span_slots(d->B, d->Hkv) * rows * (d->r_v + kSpanRowPad) * 4 + 255) & ~size_t(255);
 }
 
 int check_window(const basiskv_dims* d, int n_q, int max_seq_len, int sink, int window) {
@@ -115,12 +115,6 @@ int check_window(const basiskv_dims* d, int n_q, int max_seq_len, int sink, int 
   return BASISKV_OK;
 }
 
-// Up to kSpanMaxRows query rows a group are streamed, more go to the tensor
-// cores.
-bool window_streams(const basiskv_dims* d, int n_q) {
-  return n_q <= kSpanMaxRows / (d->Hq / d->Hkv);
-}
-
 // The mask with bounds that cover the whole context written as such.
 struct Mask {
   int sink, window;
@@ -129,10 +123,29 @@ Mask window_mask(int max_seq_len, int sink, int window) {
   return {sink < max_seq_len ? sink : max_seq_len, window < max_seq_len ? window : 0};
 }
 
+// Which calls are streamed, by the rows (query tokens times group heads) that
+// share a Key; the others go to the tensor cores, whose tiles hold 128 rows.
+// Always up to 16 rows; 17 to 32 where the call may read kStreamTokens tokens
+// or more.  Both sides, us, 7 x 8 heads and 8196 tokens, r_v 64 / 128: 20 rows
+// 53 / 62 against 78 / 143 (E4M3), 59 / 72 against 74 / 100 (bf16), 47 / 57
+// against 84 / 100 (4 bits); 32 rows 59 / 98 against 79 / 145, 72 / 104 against
+// 74 / 100, 57 / 88 against 84 / 102.  8 heads and 1028 tokens, where the code
+// itself is fetched once: 16 rows 22 / 25 against 22 / 31 (E4M3), 20 rows
+// 27 / 29 against 22 / 31, 32 rows 29 / 37 against 23 / 31.
+constexpr long long kStreamTokens = 65536;
+bool window_streams(const basiskv_dims* d, int n_q, int max_seq_len, Mask m) {
+  const int G = d->Hq / d->Hkv;
+  if (n_q <= 16 / G) return true;
+  if (n_q > kSpanMaxRows / G) return false;
+  const long long seen = (long long)m.window + n_q + m.sink;
+  const long long span = m.window > 0 && seen < max_seq_len ? seen : max_seq_len;
+  return span * d->B * d->Hkv >= kStreamTokens;
+}
+
 size_t window_bytes(const basiskv_dims* d, int n_q, int max_seq_len, int sink, int window) {
   const int G = d->Hq / d->Hkv;
-  if (window_streams(d, n_q)) return span_partial_bytes(d, n_q * G);
   const Mask m = window_mask(max_seq_len, sink, window);
+  if (window_streams(d, n_q, max_seq_len, m)) return span_partial_bytes(d, n_q * G);
   const TcPlan plan = tc_plan(d->B, d->Hkv, G, n_q, max_seq_len, m.sink, m.window);
   const size_t n = tc_partial_bytes(plan, d->r_v);
   return n > 256 ? (n + 255) & ~size_t(255) : 256;
@@ -307,6 +320,9 @@ int basiskv_cache4_attend(const basiskv_dims* dims, const basiskv_bf16* q,
   a.sel = sel;
   a.top_k = top_k;
   a.n_tot = 1;
+  // With N = B * Hkv the workspace holds (1024 + N) G (r_v + 2) partials and, behind
+  // them, N G r_v sums of the sparse decode, which this call does not make: more
+  // than the (kSpanMaxCtas + N) G (r_v + kSpanRowPad) floats that are written.
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.partial);
   return status_of(launch_span_q4(a, static_cast<cudaStream_t>(stream), pdl_allowed()));
 }
@@ -349,7 +365,7 @@ int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n
   a.n_tot = n_q;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool pdl = pdl_allowed();
-  if (window_streams(dims, n_q))
+  if (window_streams(dims, n_q, max_seq_len, m))
     return status_of(cache4 ? launch_span_q4(a, st, pdl)
                             : dims->cache_fp8 ? launch_span_e4m3(a, st, pdl)
                                               : launch_span_bf16(a, st, pdl));

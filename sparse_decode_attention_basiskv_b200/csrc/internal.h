@@ -274,7 +274,7 @@ struct SpanArgs {
   const int32_t* seq_lens;
   const int32_t* block_table;
   const int32_t* sel;  // [B][Hkv][top_k] or null
-  float* partial;      // span_slots() * rows * (r_v + 2) floats
+  float* partial;      // span_slots() * rows * (r_v + kSpanRowPad) floats
   uint16_t* out;       // [B][n_tot][Hq][r_v] bf16
   int B, Hq, Hkv, G, logG, d, r_v, S, logS, max_pages, num_phys, max_seq_len, top_k;
   int n_tot;  // query tokens per sequence, the last at position seq_lens[b] - 1
@@ -283,8 +283,9 @@ struct SpanArgs {
   float scale_log2;
   unsigned int* status;
 };
-constexpr int kSpanMaxCtas = 1024;
-constexpr int kSpanMaxRows = 16;
+constexpr int kSpanMaxCtas = 512;
+constexpr int kSpanMaxRows = 32;
+constexpr int kSpanRowPad = 4;  // floats behind a partial row's accumulators
 // CTAs of the launch for these arguments (a rule on the shape and the bound
 // max_seq_len only) and the partial slots it may write.
 inline size_t span_slots(int B, int Hkv) { return (size_t)kSpanMaxCtas + (size_t)B * Hkv; }

@@ -5,8 +5,8 @@
 //   a[row] = sum_t p_t z_t,  p = softmax over the row's tokens of
 //   (q . K_t) / sqrt(d)
 //
-// Rows: query token j and head h of KV head g make row j * G + h; 8 or 16 rows
-// (one or two N tiles of mma.m16n8k16) share every Key and latent that is
+// Rows: query token j and head h of KV head g make row j * G + h; up to 32 rows
+// (one to four N tiles of mma.m16n8k16) share every Key and latent that is
 // read.
 // Bound by HBM: 2 (d + r_v) multiply-adds a row and (d + r_v) cached columns
 // a token; over 4-bit caches closely followed by the instructions that widen
@@ -43,6 +43,14 @@
 // (2^-12 of each weight, an eighth of the output's own rounding) where the
 // operands are f16, and held as bf16 roundings plus bf16 remainders (16
 // significant bits, a second product) where they are bf16.
+//
+// Measured (16 x 32K tokens, 8 KV heads, d 128, r_v 64, G 4): bf16, window 4096
+// (202 MB) 42 us, 4.8 TB/s; 4 bits, all tokens (453 MB) 112 us, 4.0 TB/s, half of it
+// the widening's issue slots (1 in 2.4 of them a product or a conversion); 128 selected
+// pages of 4 bits (28 MB) 19 us, a start of 8 us and one turn of the ring;
+// E4M3, 7 ragged sequences, window 8192, 20 rows (89 MB) 46 us against 69 on
+// the prompt kernel.  Joining the partials of an item with one CTA took 23 us
+// longer there; one output a thread, over more CTAs, about 2.
 //
 // Formats: bf16 (bf16 products), E4M3 and 4 bits (widened to f16, which is
 // exact; each row's query is brought to f16 by a power of two that puts its
@@ -126,15 +134,19 @@ template <int FMT, int D, int RV>
 constexpr int sp_unit_bytes() {
   return sp_unit<FMT>() * (D + RV) * (FMT == kSpanBf16 ? 32 : (FMT == kSpanE4m3 ? 16 : 9)) / 16;
 }
-// CTAs an SM: two, except where the queries' and accumulators' registers (16
-// rows) or the ring (bf16) allow one.
+// CTAs an SM: two, except where the queries' and accumulators' registers (more
+// than 8 rows) or the ring (bf16) allow one.
 template <int FMT, int NR>
 constexpr int sp_ctas() {
-  return FMT == kSpanBf16 || NR == 2 ? 1 : 2;
+  return FMT == kSpanBf16 || NR >= 2 ? 1 : 2;
 }
+// The warps meet with at most 16 rows at a time.  A row: its accumulators in the
+// lanes' order (position 8 t + n: tile t, lane column n; the pad keeps the lanes'
+// writes on different banks), then maximum, sum, factor and joint sum.
+constexpr int kSpRowPad = kSpanRowPad;
 template <int FMT, int D, int RV, int NR>
 constexpr size_t sp_meet_bytes() {
-  return (size_t)kSpWarps * 8 * NR * (RV + 2) * 4;
+  return (size_t)kSpWarps * 8 * (NR < 2 ? NR : 2) * (RV + kSpRowPad) * 4;
 }
 // Ring depth: 4 units, fewer where shared memory ends (2 at least).
 template <int FMT, int D, int RV, int NR>
@@ -178,7 +190,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
   constexpr int VT = UT / 16;                      // 16-token steps
   constexpr int MT = RV / 16, KS = D / 16, NST = sp_stages<FMT, D, RV, NR>();
   constexpr int UB = sp_unit_bytes<FMT, D, RV>();
-  constexpr int RS = RV + 2;
+  constexpr int RS = RV + kSpRowPad;
   constexpr bool BULK = FMT != kSpanBf16;
   static_assert(NST >= 2 && (D + RV) * UT / 16 * 9 % 16 == 0, "");
   extern __shared__ __align__(128) uint8_t sp_smem_raw[];
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(sp_smem_raw) + warp * NST * UB;
   const uint32_t bar = smem_u32(bars + warp * NST);
-  // [warp][row][2 + RV] where the warps meet after an item
+  // [warp][row][RS] where the warps meet after an item
   float* meet = reinterpret_cast<float*>(sp_smem_raw + kSpWarps * NST * UB);
   const int R = a.n_tot * a.G;
 
@@ -773,63 +785,92 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
       }
     }
 
-    // ---- the warps meet
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
-        float* row = meet + (size_t)(warp * 8 * NR + 8 * i + 2 * c + e) * RS;
-        if (n == 0) {
-          row[0] = m[i][e];
-          row[1] = l[i][e];
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          row[2 + sp_col<FMT, RV>(2 * t, n)] = acc[t][i][e];
-          row[2 + sp_col<FMT, RV>(2 * t + 1, n)] = acc[t][i][2 + e];
-        }
-      }
-    __syncthreads();
+    // ---- the warps meet, two row tiles at a time
     float* part = a.partial + (size_t)(blockIdx.x + bg) * R * RS;
-    for (int o = tid; o < R * RV; o += kSpThreads) {
-      const int r = o / RV, col = o - r * RV;
-      float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kSpWarps; ++w) M = fmaxf(M, meet[(size_t)(w * 8 * NR + r) * RS]);
-      float L = 0.f, A = 0.f;
+    for (int i0 = 0; i0 < NR; i0 += 2) {
+      constexpr int MR = 8 * (NR < 2 ? NR : 2);
 #pragma unroll
-      for (int w = 0; w < kSpWarps; ++w) {
-        const float* row = meet + (size_t)(w * 8 * NR + r) * RS;
-        const float f = row[0] == -INFINITY ? 0.f : ex2(row[0] - M);
-        L = fmaf(row[1], f, L);
-        A = fmaf(row[2 + col], f, A);
-      }
-      if (alone) {
-        const int j = r / a.G, h = r - j * a.G;
-        a.out[(((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV + col] =
-            f_to_bf16(L > 0.f ? A / L : 0.f);
-      } else {
-        part[r * RS + 2 + col] = A;
-        if (col == 0) {
-          part[r * RS] = M;
-          part[r * RS + 1] = L;
+      for (int i = i0; i < i0 + 2 && i < NR; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
+          float* row = meet + (size_t)(warp * MR + 8 * (i - i0) + 2 * c + e) * RS;
+          if (n == 0) {
+            row[RV] = m[i][e];
+            row[RV + 1] = l[i][e];
+          }
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            row[16 * t + n] = acc[t][i][e];
+            row[16 * t + 8 + n] = acc[t][i][2 + e];
+          }
+        }
+      __syncthreads();
+      const int rows = min(R - 8 * i0, MR);
+      if (tid < kSpWarps * MR) {  // the warps' factors, the joint maximum and sum
+        const int w = tid / MR, rr = tid - w * MR;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int x = 0; x < kSpWarps; ++x) M = fmaxf(M, meet[(size_t)(x * MR + rr) * RS + RV]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float* row = meet + (size_t)(w * MR + rr) * RS;
+        row[RV + 2] = ex2(row[RV] - ref);
+        if (w == 0) {
+#pragma unroll
+          for (int x = 0; x < kSpWarps; ++x) {
+            const float* other = meet + (size_t)(x * MR + rr) * RS;
+            L = fmaf(other[RV + 1], ex2(other[RV] - ref), L);
+          }
+          row[RV + 3] = L;
+          if (!alone && rr < rows) {
+            part[(8 * i0 + rr) * RS + RV] = M;
+            part[(8 * i0 + rr) * RS + RV + 1] = L;
+          }
         }
       }
+      __syncthreads();
+      for (int o = tid; o < rows * (RV / 4); o += kSpThreads) {
+        const int rr = o / (RV / 4), at = 4 * (o - rr * (RV / 4)), r = 8 * i0 + rr;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kSpWarps; ++w) {
+          const float* row = meet + (size_t)(w * MR + rr) * RS;
+          const float4 x = *reinterpret_cast<const float4*>(row + at);
+          const float f = row[RV + 2];
+          A.x = fmaf(x.x, f, A.x);
+          A.y = fmaf(x.y, f, A.y);
+          A.z = fmaf(x.z, f, A.z);
+          A.w = fmaf(x.w, f, A.w);
+        }
+        if (alone) {
+          const float L = meet[(size_t)rr * RS + RV + 3], inv = L > 0.f ? 1.f / L : 0.f;
+          const int j = r / a.G, h = r - j * a.G;
+          uint16_t* dst = a.out + (((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV;
+          const float v[4] = {A.x * inv, A.y * inv, A.z * inv, A.w * inv};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            dst[sp_col<FMT, RV>(at >> 3, (at & 7) + x)] = f_to_bf16(v[x]);
+        } else {
+          *reinterpret_cast<float4*>(part + r * RS + at) = A;
+        }
+      }
+      __syncthreads();  // the meeting place is free again
     }
-    __syncthreads();  // the meeting place is free again
     seg = item_end;
   }
 }
 
 // Joins the partials of the items that several CTAs share; rows of items
-// without units are zero.  One CTA per (sequence, KV head).  The lengths are
-// read before the grid-dependency wait: the launch before this one let it in
-// after its own wait, and does not write them.
-template <int UT, int RV>
+// without units are zero.  A thread joins one output: CTA (x, y) has outputs
+// 256 y .. of (sequence, KV head) x, so the joins of a few items are not one
+// CTA's chain of loads.  The lengths are read before the grid-dependency wait:
+// the launch before this one let it in after its own wait, and does not write
+// them.
+template <int FMT, int RV>
 __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int grid) {
-  constexpr int RS = RV + 2;
+  constexpr int RS = RV + kSpRowPad, UT = sp_unit<FMT>();
   __shared__ long long pre[257];
   span_scan<UT>(a, pre, false);
   const int bg = blockIdx.x, b = bg / a.Hkv, g = bg - b * a.Hkv, R = a.n_tot * a.G;
@@ -841,27 +882,24 @@ __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int 
     c0 = span_cta_of(x0, total, C);
     c1 = span_cta_of(x0 + u - 1, total, C);
   }
+  const int o = blockIdx.y * kSpThreads + threadIdx.x, r = o / RV, at = o - r * RV;
   pdl_wait();
   pdl_launch_dependents();
-  if (u > 0 && c0 == c1) return;  // written by its one CTA
-  for (int o = threadIdx.x; o < R * RV; o += kSpThreads) {
-    const int r = o / RV, col = o - r * RV;
-    float M = -INFINITY, L = 0.f, A = 0.f;
+  if ((u > 0 && c0 == c1) || r >= R) return;  // written by its one CTA
+  float M = -INFINITY, L = 0.f, A = 0.f;
 #pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-      const float* s = a.partial + ((size_t)(c + bg) * R + r) * RS;
-      const float mc = __ldcg(s), lc = __ldcg(s + 1), ac = __ldcg(s + 2 + col);
-      if (mc == -INFINITY) continue;
-      const float mn = fmaxf(M, mc);
-      const float f0 = M == -INFINITY ? 0.f : ex2(M - mn), f1 = ex2(mc - mn);
-      L = fmaf(L, f0, lc * f1);
-      A = fmaf(A, f0, ac * f1);
-      M = mn;
-    }
-    const int j = r / a.G, h = r - j * a.G;
-    a.out[(((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV + col] =
-        f_to_bf16(L > 0.f ? A / L : 0.f);
+  for (int c = c0; c <= c1; ++c) {
+    const float* s = a.partial + ((size_t)(c + bg) * R + r) * RS;
+    const float mc = __ldcg(s + RV), lc = __ldcg(s + RV + 1), ac = __ldcg(s + at);
+    const float mn = fmaxf(M, mc);
+    const float f0 = M == -INFINITY ? 0.f : ex2(M - mn), f1 = mc == -INFINITY ? 0.f : ex2(mc - mn);
+    L = fmaf(L, f0, lc * f1);
+    A = fmaf(A, f0, ac * f1);
+    M = mn;
   }
+  const int j = r / a.G, h = r - j * a.G, col = sp_col<FMT, RV>(at >> 3, at & 7);
+  a.out[(((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV + col] =
+      f_to_bf16(L > 0.f ? A / L : 0.f);
 }
 
 template <int FMT, int D, int RV, int NR, bool ONE = false>
@@ -885,27 +923,25 @@ cudaError_t launch_span_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
   e = launch_k(span_kernel<FMT, D, RV, NR, ONE>, dim3((unsigned)grid), dim3(kSpThreads), smem, st, pdl,
                a);
   if (e != cudaSuccess) return e;
-  return launch_k(span_merge_kernel<UT, RV>, dim3(a.B * a.Hkv), dim3(kSpThreads), 0, st, pdl, a,
-                  (int)grid);
+  const int outs = a.n_tot * a.G * RV;
+  return launch_k(span_merge_kernel<FMT, RV>, dim3(a.B * a.Hkv, (outs + kSpThreads - 1) / kSpThreads),
+                  dim3(kSpThreads), 0, st, pdl, a, (int)grid);
 }
 
 template <int FMT, bool ONE = false>
 cudaError_t launch_span_fmt(const SpanArgs& a, cudaStream_t st, bool pdl) {
-  const bool two = a.n_tot * a.G > 8;
-#define BKV_SPAN_RV(DD)                                                       \
-  switch (a.r_v) {                                                            \
-    case 32:                                                                  \
-      return two ? launch_span_t<FMT, DD, 32, 2, ONE>(a, st, pdl)             \
-                 : launch_span_t<FMT, DD, 32, 1, ONE>(a, st, pdl);            \
-    case 64:                                                                  \
-      return two ? launch_span_t<FMT, DD, 64, 2, ONE>(a, st, pdl)             \
-                 : launch_span_t<FMT, DD, 64, 1, ONE>(a, st, pdl);            \
-    case 96:                                                                  \
-      return two ? launch_span_t<FMT, DD, 96, 2, ONE>(a, st, pdl)             \
-                 : launch_span_t<FMT, DD, 96, 1, ONE>(a, st, pdl);            \
-    default:                                                                  \
-      return two ? launch_span_t<FMT, DD, 128, 2, ONE>(a, st, pdl)            \
-                 : launch_span_t<FMT, DD, 128, 1, ONE>(a, st, pdl);           \
+  const int tiles = (a.n_tot * a.G + 7) / 8;  // of 8 rows
+#define BKV_SPAN_NR(DD, RR)                                                  \
+  return tiles == 1   ? launch_span_t<FMT, DD, RR, 1, ONE>(a, st, pdl)       \
+         : tiles == 2 ? launch_span_t<FMT, DD, RR, 2, ONE>(a, st, pdl)       \
+         : tiles == 3 ? launch_span_t<FMT, DD, RR, 3, ONE>(a, st, pdl)       \
+                      : launch_span_t<FMT, DD, RR, 4, ONE>(a, st, pdl)
+#define BKV_SPAN_RV(DD)                                                      \
+  switch (a.r_v) {                                                           \
+    case 32: BKV_SPAN_NR(DD, 32);                                            \
+    case 64: BKV_SPAN_NR(DD, 64);                                            \
+    case 96: BKV_SPAN_NR(DD, 96);                                            \
+    default: BKV_SPAN_NR(DD, 128);                                           \
   }
   if (a.d == 64) {
     BKV_SPAN_RV(64)
@@ -913,6 +949,7 @@ cudaError_t launch_span_fmt(const SpanArgs& a, cudaStream_t st, bool pdl) {
     BKV_SPAN_RV(128)
   }
 #undef BKV_SPAN_RV
+#undef BKV_SPAN_NR
 }
 
 }  // namespace

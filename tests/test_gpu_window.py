@@ -53,9 +53,9 @@ class Problem:
                                   cache4=self.fmt == "4bit")
         return out
 
-    def check(self, out=None):
+    def check(self, out=None, kind=None):
         got = (self.out if out is None else out).cpu().double().numpy()
-        kind = self.fmt
+        kind = kind or self.fmt
         if kind == "bf16":
             kind = "bf16_token" if self.n * self.G <= 16 else "bf16_prompt"
         for b, L in enumerate(self.lens):
@@ -147,6 +147,20 @@ def test_growing_scores(fmt):
 ])
 def test_prompts(fmt, B, G, Hkv, n, lens):
     _go(fmt, B, G, Hkv, 64, 64, 16, lens, n, 0 if n % 2 else 250, 4)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("window,sink", [(0, 0), (1024, 5)])
+@pytest.mark.parametrize("G,d,rv,page,n", [(4, 128, 64, 16, 5), (8, 64, 96, 32, 3),
+                                           (8, 128, 128, 32, 4), (1, 64, 128, 16, 31),
+                                           (4, 64, 64, 32, 7), (2, 128, 32, 16, 9)])
+def test_streamed_drafts(fmt, window, sink, G, d, rv, page, n):
+    """17 to 32 rows a group over 64 contexts of a thousand tokens and more."""
+    p = Problem(fmt, 8, G, 8, d, rv, page, [1300, 3, 0, 17, 1100, 1029, 900, 1301], n, window,
+                sink)
+    p.run()
+    assert bkv.read_device_status() == 0
+    p.check(kind="bf16_token" if fmt == "bf16" else fmt)
 
 
 def test_many_items():
