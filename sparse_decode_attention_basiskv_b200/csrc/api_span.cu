@@ -127,8 +127,8 @@ Mask window_mask(int max_seq_len, int sink, int window) {
 // share a Key; the others go to the tensor cores, whose tiles hold 128 rows.
 // Always up to 16 rows; 17 to 32 where the call may read kStreamTokens tokens
 // or more.  Both sides, us, 7 x 8 heads and 8196 tokens, r_v 64 / 128: 20 rows
-// 53 / 62 against 78 / 143 (E4M3), 59 / 72 against 74 / 100 (bf16), 47 / 57
-// against 84 / 100 (4 bits); 32 rows 59 / 98 against 79 / 145, 72 / 104 against
+// 51 / 59 against 78 / 143 (E4M3), 59 / 72 against 74 / 100 (bf16), 47 / 57
+// against 84 / 100 (4 bits); 32 rows 57 / 92 against 79 / 145, 72 / 104 against
 // 74 / 100, 57 / 88 against 84 / 102.  8 heads and 1028 tokens, where the code
 // itself is fetched once: 16 rows 22 / 25 against 22 / 31 (E4M3), 20 rows
 // 27 / 29 against 22 / 31, 32 rows 29 / 37 against 23 / 31.
@@ -137,6 +137,7 @@ bool window_streams(const basiskv_dims* d, int n_q, int max_seq_len, Mask m) {
   const int G = d->Hq / d->Hkv;
   if (n_q <= 16 / G) return true;
   if (n_q > kSpanMaxRows / G) return false;
+  if (d->cache_fp8 && d->page_size < 16) return false;  // two pages of 16 make a unit there
   const long long seen = (long long)m.window + n_q + m.sink;
   const long long span = m.window > 0 && seen < max_seq_len ? seen : max_seq_len;
   return span * d->B * d->Hkv >= kStreamTokens;

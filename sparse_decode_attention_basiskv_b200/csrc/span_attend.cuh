@@ -48,7 +48,7 @@
 // (202 MB) 42 us, 4.8 TB/s; 4 bits, all tokens (453 MB) 112 us, 4.0 TB/s, half of it
 // the widening's issue slots (1 in 2.4 of them a product or a conversion); 128 selected
 // pages of 4 bits (28 MB) 19 us, a start of 8 us and one turn of the ring;
-// E4M3, 7 ragged sequences, window 8192, 20 rows (89 MB) 46 us against 69 on
+// E4M3, 7 ragged sequences, window 8192, 20 rows (89 MB) 43 us against 69 on
 // the prompt kernel.  Joining the partials of an item with one CTA took 23 us
 // longer there; one output a thread, over more CTAs, about 2.
 //
@@ -76,10 +76,12 @@ constexpr float sp_slack() {
   return FMT == kSpanBf16 ? 64.f : 15.f;
 }
 
-// Tokens of a unit.
-template <int FMT>
+// Tokens of a unit: 32 over 4-bit caches, and over E4M3 ones where 17 to 32 rows
+// leave a warp a scheduler and a half (two steps of 16 tokens side by side: 46
+// -> 43 us with 20 rows over 89 MB; pages of 8 tokens are not halves of such a unit).
+template <int FMT, int NR>
 constexpr int sp_unit() {
-  return FMT == kSpanQ4 ? 32 : 16;
+  return FMT == kSpanQ4 || (FMT == kSpanE4m3 && NR > 2) ? 32 : 16;
 }
 
 // What one sequence contributes: its live length, and the units of one KV
@@ -130,9 +132,9 @@ __device__ __forceinline__ int span_cta_of(long long x, long long total, int C) 
 }
 
 // Bytes of one unit in a warp's ring, and of the ring's part of shared memory.
-template <int FMT, int D, int RV>
+template <int FMT, int D, int RV, int NR>
 constexpr int sp_unit_bytes() {
-  return sp_unit<FMT>() * (D + RV) * (FMT == kSpanBf16 ? 32 : (FMT == kSpanE4m3 ? 16 : 9)) / 16;
+  return sp_unit<FMT, NR>() * (D + RV) * (FMT == kSpanBf16 ? 32 : (FMT == kSpanE4m3 ? 16 : 9)) / 16;
 }
 // CTAs an SM: two, except where the queries' and accumulators' registers (more
 // than 8 rows) or the ring (bf16) allow one.
@@ -152,12 +154,12 @@ constexpr size_t sp_meet_bytes() {
 template <int FMT, int D, int RV, int NR>
 constexpr int sp_stages() {
   const size_t room = 224 * 1024 / sp_ctas<FMT, NR>() - 6 * 1024 - sp_meet_bytes<FMT, D, RV, NR>();
-  const size_t n = room / ((size_t)kSpWarps * sp_unit_bytes<FMT, D, RV>());
+  const size_t n = room / ((size_t)kSpWarps * sp_unit_bytes<FMT, D, RV, NR>());
   return n < 4 ? (int)n : 4;
 }
 template <int FMT, int D, int RV, int NR>
 constexpr size_t sp_smem() {
-  return (size_t)kSpWarps * sp_stages<FMT, D, RV, NR>() * sp_unit_bytes<FMT, D, RV>() +
+  return (size_t)kSpWarps * sp_stages<FMT, D, RV, NR>() * sp_unit_bytes<FMT, D, RV, NR>() +
          sp_meet_bytes<FMT, D, RV, NR>();
 }
 
@@ -186,10 +188,10 @@ __device__ __forceinline__ void mbar_arrive_only(uint32_t bar) {
 // ONE (4-bit caches): a unit is one page of 32 tokens, else two of 16.
 template <int FMT, int D, int RV, int NR, bool ONE>
 __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(SpanArgs a) {
-  constexpr int UT = sp_unit<FMT>(), HT = UT / 2;  // tokens of a unit, of its halves
+  constexpr int UT = sp_unit<FMT, NR>(), HT = UT / 2;  // tokens of a unit, of its halves
   constexpr int VT = UT / 16;                      // 16-token steps
   constexpr int MT = RV / 16, KS = D / 16, NST = sp_stages<FMT, D, RV, NR>();
-  constexpr int UB = sp_unit_bytes<FMT, D, RV>();
+  constexpr int UB = sp_unit_bytes<FMT, D, RV, NR>();
   constexpr int RS = RV + kSpRowPad;
   constexpr bool BULK = FMT != kSpanBf16;
   static_assert(NST >= 2 && (D + RV) * UT / 16 * 9 % 16 == 0, "");
@@ -323,9 +325,9 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
               copy(st + at * D, a.K + (size_t)row * D, rows * D);
               const uint8_t* tile = a.Z + (size_t)(row >> a.logS) * a.S * RV;
               const int r = row & (a.S - 1);
-              copy(st + 16 * D + at * F, tile + r * F, rows * F);
+              copy(st + UT * D + at * F, tile + r * F, rows * F);
               if (F < RV)
-                copy(st + 16 * D + 16 * F + at * (RV - F), tile + a.S * F + r * (RV - F),
+                copy(st + UT * D + UT * F + at * (RV - F), tile + a.S * F + r * (RV - F),
                      rows * (RV - F));
             };
             if (a.S >= UT && present == 2) {
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
               const int F = a.zsplit;
 #pragma unroll
               for (int k = 0; k < RV; k += 16) {
-                const uint32_t at = zs + (k < F ? lane * F + k : 16 * F + lane * (RV - F) + k - F);
+                const uint32_t at = zs + (k < F ? lane * F + k : UT * F + lane * (RV - F) + k - F);
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u)
                              : "memory");
               }
@@ -565,19 +567,21 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
         }
       } else if constexpr (FMT == kSpanE4m3) {
 #pragma unroll
-        for (int k4 = 0; k4 < KS / 4; ++k4) {
-          // 16 columns of tokens n and n + 8
-          const uint4 x = lds128(ks + n * D + (c + 4 * k4) * 16);
-          const uint4 y = lds128(ks + (n + 8) * D + (c + 4 * k4) * 16);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        for (int k4 = 0; k4 < KS / 4; ++k4)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16(xw[w], a0, a2);
-            e4m3x4_to_f16(yw[w], a1, a3);
-            qk(0, 4 * k4 + w, a0, a1, a2, a3);
+          for (int v = 0; v < VT; ++v) {
+            // 16 columns of tokens n and n + 8
+            const uint4 x = lds128(ks + (16 * v + n) * D + (c + 4 * k4) * 16);
+            const uint4 y = lds128(ks + (16 * v + n + 8) * D + (c + 4 * k4) * 16);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(xw[w], a0, a2);
+              e4m3x4_to_f16(yw[w], a1, a3);
+              qk(v, 4 * k4 + w, a0, a1, a2, a3);
+            }
           }
-        }
       } else {
         // D / 4 columns of tokens n and n + 8: D / 8 bytes, one scale per 16
         const uint32_t kl = ks + lane_k, kls = ks + lane_ks;
@@ -766,8 +770,8 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
 #pragma unroll
           for (int w = 0; w < RV / 32; ++w) {
             const int col = 32 * w + 4 * n;
-            const uint32_t at = zs + (col < F ? col : 16 * F + col - F);
             const int pitch = col < F ? F : RV - F;
+            const uint32_t at = zs + (col < F ? col : UT * F + col - F) + 16 * v * pitch;
             uint32_t x[4], f[2][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -868,9 +872,9 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
 // CTA's chain of loads.  The lengths are read before the grid-dependency wait:
 // the launch before this one let it in after its own wait, and does not write
 // them.
-template <int FMT, int RV>
+template <int FMT, int RV, int UT>
 __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int grid) {
-  constexpr int RS = RV + kSpRowPad, UT = sp_unit<FMT>();
+  constexpr int RS = RV + kSpRowPad;
   __shared__ long long pre[257];
   span_scan<UT>(a, pre, false);
   const int bg = blockIdx.x, b = bg / a.Hkv, g = bg - b * a.Hkv, R = a.n_tot * a.G;
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int 
 
 template <int FMT, int D, int RV, int NR, bool ONE = false>
 cudaError_t launch_span_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
-  constexpr int UT = sp_unit<FMT>();
+  constexpr int UT = sp_unit<FMT, NR>();
   // Units of the longest context this call may meet; fewer CTAs when they do
   // not suffice for kSpMinUnits each.
   long long most = (long long)a.max_seq_len + UT;
@@ -924,7 +928,7 @@ cudaError_t launch_span_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
                a);
   if (e != cudaSuccess) return e;
   const int outs = a.n_tot * a.G * RV;
-  return launch_k(span_merge_kernel<FMT, RV>, dim3(a.B * a.Hkv, (outs + kSpThreads - 1) / kSpThreads),
+  return launch_k(span_merge_kernel<FMT, RV, UT>, dim3(a.B * a.Hkv, (outs + kSpThreads - 1) / kSpThreads),
                   dim3(kSpThreads), 0, st, pdl, a, (int)grid);
 }
 

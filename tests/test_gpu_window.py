@@ -163,6 +163,12 @@ def test_streamed_drafts(fmt, window, sink, G, d, rv, page, n):
     p.check(kind="bf16_token" if fmt == "bf16" else fmt)
 
 
+def test_drafts_over_small_pages():
+    """Pages of 8 tokens in the sizes that are streamed otherwise."""
+    for fmt in ("bf16", "e4m3"):
+        _go(fmt, 8, 4, 8, 128, 64, 8, [1100, 3, 0, 17, 1029, 1040, 900, 1101], 6, 0, 0)
+
+
 def test_many_items():
     """More items than SMs: whole ones, and a last round that is cut into runs."""
     p = _go("bf16", 5, 8, 4, 64, 32, 16, [300, 290, 310, 280, 305], 260, 200, 4)
