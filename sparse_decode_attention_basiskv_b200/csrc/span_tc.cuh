@@ -63,6 +63,12 @@ struct TcGeom {
   static constexpr int kZBlocks = (RV + 63) / 64;  // 64-column blocks
   static constexpr int kZBytes = kZBlocks * 128 * 128;
   static constexpr int kStages = RV <= 64 ? 3 : 2;
+  // k-steps of Q whose A operand lies in tensor memory (32 columns hold 4)
+  static constexpr int kRoom = (128 - RV) / 32 * 4;
+  static constexpr int kQSteps = kRoom < D / 16 ? kRoom : D / 16;
+  // its columns: S of row tile t at 128 t, then O, then Q
+  static constexpr int kO = 256, kQ = kO + 2 * RV;
+  static_assert(kQ + 16 * kQSteps <= 512, "");
   static constexpr size_t kSmem = 1024 + kQBytes + kStages * (size_t)(kKBytes + kZBytes);
 };
 
@@ -238,7 +244,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
       constexpr uint32_t id_pv = tc_idesc(128, RV, BF, true);
       const uint64_t dq = tc_sdesc(sq + t * (Gm::kQBytes / 2)), dk = tc_sdesc(sk),
                      dz = tc_sdesc(sz, 16384);
-      const uint32_t tm_s = tmem + 128 * t, tm_o = tmem + 256 + 128 * t;
+      const uint32_t tm_s = tmem + 128 * t, tm_o = tmem + Gm::kO + RV * t;
+      const uint32_t tm_q = tmem + Gm::kQ + 8 * Gm::kQSteps * t;
       const bool lead = elect_one();
       auto wait = [&](uint64_t* bar, int parity) {
         return mbar_poll(bar, parity, a.status, abrt);
@@ -249,9 +256,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
         if (lead) {
           const uint64_t k0 = dk + st * (Gm::kKBytes >> 4) + (u & 1) * (64 * 128 >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma_ss(tm_s + 64 * (u & 1), dq + (k >> 2) * 1024 + (k & 3) * 2,
-                      k0 + (k >> 2) * 1024 + (k & 3) * 2, id_qk, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t kk = k0 + (k >> 2) * 1024 + (k & 3) * 2;
+            if (k < Gm::kQSteps)
+              tc_mma_ts(tm_s + 64 * (u & 1), tm_q + 8 * k, kk, id_qk, k > 0);
+            else
+              tc_mma_ss(tm_s + 64 * (u & 1), dq + (k >> 2) * 1024 + (k & 3) * 2, kk, id_qk, k > 0);
+          }
           tc_commit_to(&sfull[2 * t + (u & 1)]);
           if (u & 1) tc_commit_to(&kempty[st]);
         }
@@ -516,12 +527,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
         }
       }
       fence_proxy_async();
-      arrive_warp(qfull);
-      if (!BF) named_bar_sync(1, 256);  // row_scale
+      if (!BF || Gm::kQSteps > 0) named_bar_sync(1, 256);  // the rows and row_scale
     }
     const int t = (warp >> 2) - 1, r = tid & 127, row = t * 128 + r;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
+    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + Gm::kO + RV * t;
+    if constexpr (Gm::kQSteps > 0) {  // the thread's row, from shared to tensor memory
+      const uint32_t tq = tmem + lanes + Gm::kQ + 8 * Gm::kQSteps * t;
+#pragma unroll
+      for (int x = 0; x < Gm::kQSteps / 4; ++x) {
+        uint32_t u[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = lds128(sq + t * (Gm::kQBytes / 2) + tc_off(r, 8 * x + c));
+          u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
+        }
+        tc_st32(tq + 32 * x, u);
+      }
+      tc_wait_st();
+      tc_fence_before_sync();
+    }
+    arrive_warp(qfull);
     if (t < nt) {
       const int j = row >> a.logG, h = row & (a.G - 1);
       const bool live = row < rows;
