@@ -164,13 +164,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
   constexpr bool BF = FMT == kSpanBf16;
   extern __shared__ uint8_t tc_smem_raw[];
   uint8_t* smem = align_smem_1k(tc_smem_raw);
-  __shared__ uint64_t bars[4 * NST + 13];
+  __shared__ uint64_t bars[4 * NST + 9];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float row_scale[kTcRows];
   uint64_t *kfull = bars, *kempty = bars + NST, *zfull = bars + 2 * NST, *zempty = bars + 3 * NST;
-  // [row tile][slot]: S is there, P is there, O has the step
-  uint64_t *sfull = bars + 4 * NST, *pfull = sfull + 4, *ofull = sfull + 8, *qfull = sfull + 12;
+  // [row tile][slot]: S of step u is there and O has step u - 2 (two phases more
+  // than there are steps); P is there
+  uint64_t *sfull = bars + 4 * NST, *pfull = sfull + 4, *qfull = sfull + 8;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const uint32_t sq = smem_u32(smem), sk = sq + Gm::kQBytes, sz = sk + NST * Gm::kKBytes;
@@ -192,7 +193,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
     for (int t = 0; t < 4; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pfull[t], 4);
-      mbar_init(&ofull[t], 1);
     }
     mbar_init(qfull, 8);
     abort_flag = 0;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + k * 128, id_pv, u > 0 || k > 0);
-          tc_commit_to(&ofull[2 * t + (u & 1)]);
+          if (u + 2 >= n2) tc_commit_to(&sfull[2 * t + (u & 1)]);
           if (u & 1) tc_commit_to(&zempty[zst]);
         }
         __syncwarp();
@@ -563,41 +563,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
       for (int u = 0; u < n2; ++u) {
         const uint32_t tu = ts + 64 * (u & 1);
         ok = mbar_poll(&sfull[2 * t + (u & 1)], (u >> 1) & 1, a.status, abrt);
-        // No phase of `ofull` is skipped, so a wait's parity names one phase (step
-        // u - 2 is multiplied by now, but its arrival may be seen after S's).
-        if (u > 1) ok = mbar_poll(&ofull[2 * t + (u & 1)], ((u >> 1) - 1) & 1, a.status, abrt) && ok;
         if (!ok) break;
         tc_fence_after_sync();
-        uint32_t sa[32], sb[32], p[32];
-        tc_ld32(tu, sa);
-        tc_ld32(tu + 32, sb);
         const int t0 = tc_tile(it, i0 + (u >> 1)) * 128 + 64 * (u & 1);
-        tc_wait_ld(sa);
-        tc_wait_ld(sb);
-        if (!(t0 + 63 <= pos_a && (t0 >= lo_b || t0 + 63 < a.sink))) {
-          // column x holds token t0 + x: visible up to pos, from lo on or below
-          // the sinks' end
-          const int me = pos - t0, mf = lo - t0, mg = a.sink - t0;
+        const bool all_seen = t0 + 63 <= pos_a && (t0 >= lo_b || t0 + 63 < a.sink);
+        uint32_t p[32];
+        uint64_t sum;
+        // The weights are taken against the reference at hand, with the maximum on
+        // the side; where a row has outgrown it, the warp moves it and reads S again.
+#pragma unroll 1
+        for (int pass = 0; ok; ++pass) {
+          uint32_t sa[32], sb[32];
+          tc_ld32(tu, sa);
+          tc_ld32(tu + 32, sb);
+          tc_wait_ld(sa);
+          tc_wait_ld(sb);
+          if (!all_seen) {
+            // column x holds token t0 + x: visible up to pos, from lo on or below
+            // the sinks' end
+            const int me = pos - t0, mf = lo - t0, mg = a.sink - t0;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            if (x > me || (x < mf && x >= mg)) sa[x] = 0xff800000u;
-            if (x + 32 > me || (x + 32 < mf && x + 32 >= mg)) sb[x] = 0xff800000u;
+            for (int x = 0; x < 32; ++x) {
+              if (x > me || (x < mf && x >= mg)) sa[x] = 0xff800000u;
+              if (x + 32 > me || (x + 32 < mf && x + 32 >= mg)) sb[x] = 0xff800000u;
+            }
           }
-        }
-        float mx = -INFINITY, my = -INFINITY;
+          const uint32_t nb = __float_as_uint(m == -INFINITY ? 0.f : -m);
+          const uint64_t nbase = pack2(nb, nb);
+          float mx = -INFINITY;
+          sum = 0;
+          auto weights = [&](const uint32_t (&s)[32], uint32_t* out) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          mx = max3(mx, __uint_as_float(sa[x]), __uint_as_float(sa[x + 1]));
-          my = max3(my, __uint_as_float(sb[x]), __uint_as_float(sb[x + 1]));
-        }
-        mx = fmaxf(mx, my) * sl;
-        const bool grow = u == 0 || mx > m + tc_slack<FMT>();
-        if (__any_sync(0xffffffffu, grow)) {
+            for (int y = 0; y < 32; y += 2) {
+              float p0, p1;
+              unpack2(fma2(pack2(s[y], s[y + 1]), sl2, nbase), p0, p1);
+              mx = max3(mx, __uint_as_float(s[y]), __uint_as_float(s[y + 1]));
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum = add2(sum, pack2(__float_as_uint(p0), __float_as_uint(p1)));
+              if constexpr (BF) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+                out[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
+              } else {
+                const __half2 v = __floats2half2_rn(p0, p1);
+                out[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+            }
+          };
+          weights(sa, p);
+          weights(sb, p + 16);
+          mx *= sl;
+          const bool grow = mx > m + tc_slack<FMT>();
+          if (pass > 0 || !__any_sync(0xffffffffu, grow)) break;
           const float f = grow ? ex2(m - mx) : 1.f;
           if (grow) m = mx;
-          if (u > 0) {  // O is complete up to the step before this one
+          if (u > 0) {
             l *= f;
-            ok = mbar_poll(&ofull[2 * t + ((u - 1) & 1)], ((u - 1) >> 1) & 1, a.status, abrt);
+            // the next S comes behind P Z of the step before this one
+            ok = mbar_poll(&sfull[2 * t + ((u + 1) & 1)], ((u + 1) >> 1) & 1, a.status, abrt);
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll 1
@@ -610,28 +633,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
             }
           }
         }
-        const uint32_t nb = __float_as_uint(m == -INFINITY ? 0.f : -m);
-        const uint64_t nbase = pack2(nb, nb);
-        uint64_t sum = 0;
-        auto weights = [&](const uint32_t (&s)[32], uint32_t* out) {
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            float p0, p1;
-            unpack2(fma2(pack2(s[y], s[y + 1]), sl2, nbase), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum = add2(sum, pack2(__float_as_uint(p0), __float_as_uint(p1)));
-            if constexpr (BF) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
-              out[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
-            } else {
-              const __half2 v = __floats2half2_rn(p0, p1);
-              out[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-          }
-        };
-        weights(sa, p);
-        weights(sb, p + 16);
+        if (!ok) break;
         tc_st32(tu, p);  // over the first 32 columns of S
         float sum0, sum1;
         unpack2(sum, sum0, sum1);
@@ -640,7 +642,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
         tc_fence_before_sync();
         arrive_warp(&pfull[2 * t + (u & 1)]);
       }
-      if (n > 0 && ok) ok = mbar_poll(&ofull[2 * t + ((n2 - 1) & 1)], ((n2 - 1) >> 1) & 1, a.status, abrt);
+      if (n2 > 1 && ok) ok = mbar_poll(&sfull[2 * t + (n2 & 1)], (n2 >> 1) & 1, a.status, abrt);
+      if (n2 > 0 && ok)
+        ok = mbar_poll(&sfull[2 * t + ((n2 + 1) & 1)], ((n2 + 1) >> 1) & 1, a.status, abrt);
       if (ok) {
         tc_fence_after_sync();
         const float inv = l > 0.f ? 1.f / l : 0.f;
