@@ -13,8 +13,8 @@ using namespace basiskv;
 
 // Rounds of the SMs take whole items while they are full.  What is left over is
 // cut so that the rounds it takes are short and few: a run costs its KV tiles
-// and about 5 tiles' time for its start and end (measured: 13,000 and 3,100
-// clocks), and keeps 4 tiles at least.
+// and about 5 tiles' time for its start and end (measured: 16,000 and 3,500
+// clocks at d 128, r_v 64), and keeps 4 tiles at least.
 TcPlan basiskv::tc_plan(int B, int Hkv, int G, int n_tot, int max_seq_len, int sink, int window) {
   const int sms = num_sms(), tq2 = 256 / G;
   const long long items = (long long)B * Hkv * ((n_tot + tq2 - 1) / tq2);

@@ -10,11 +10,12 @@
 // token and a head of the group (token-major), so the group's heads share each
 // Key and latent that is loaded, and a tile spans only 128 / G tokens of the
 // band.  KV comes in tiles of 128 tokens and is multiplied in steps of 64: per
-// step and row tile S = Q K^T (tcgen05, both operands in shared memory),
-// P = exp2(S - m) (registers), O += P Z (A from tensor memory).  Two row tiles
-// and 128 tokens take 2 * 128 * 128 * (d + r_v) multiply-adds and 2 * 128 * 128
-// exponentials: at d 128, r_v 64 the tensor cores need 2100 clocks (a 128 x 64
-// x 16 product takes 49, not 32) and the 16 exponentials a clock 2050.
+// step and row tile S = Q K^T (tcgen05), P = exp2(S - m) (registers), O += P Z,
+// Q and P as A operands in tensor memory.  Two row tiles and 128 tokens take
+// 2 * 128 * 128 * (d + r_v) multiply-adds and 2 * 128 * 128 exponentials: at d
+// 128, r_v 64 the tensor cores need 1600 clocks (a 128 x 64 x 16 product takes
+// 33; 49 with both operands in shared memory, whose bandwidth then bounds it)
+// and the 16 exponentials a clock 2050.
 //
 // Roles (16 warps, one CTA an SM): warps 0 and 1 issue the MMAs of one row tile
 // each; warps 4-7 and 8-11 hold the softmax of one row tile each, a thread a
@@ -26,11 +27,23 @@
 // ahead of what they hand over.
 //
 // Tensor memory: per row tile two slots of 64 columns for S, P over the first
-// 32 of its S, and 128 for O.  Q K^T of step i + 2 follows P Z of step i on the
-// tensor cores into the same slot, while the softmax has step i + 1 before it,
-// so its latency is hidden.  (One slot of 128 columns a row tile, the softmax
-// waiting for each product, took 300 us where this takes 280, at a
-// 4096-token chunk of the Llama-8B layer over a window of 4096, bf16.)
+// 32 of its S, r_v for O, and Q in what is left (all of it for r_v up to 64, d
+// 128; the other k-steps read Q from shared memory).  Q K^T of step i + 2
+// follows P Z of step i on the tensor cores into the same slot, while the
+// softmax has step i + 1 before it, so its latency is hidden.  A product's end
+// needs no barrier of its own: S of step i + 2 is behind P Z of step i, so its
+// barrier tells both (a wait costs some 270 clocks even when the phase is
+// over; one a step less took the chunk below from 305 to 282 us).
+//
+// Measured (4096-token chunk, Llama-8B layer, window 4096, bf16): 282 us, 731
+// TFLOP/s.  Three ragged sequences of 1023 tokens, Qwen3-32B layer, window
+// 2000, 4 bits: 274 us, 643 TFLOP/s.  Bound by the softmax's chain of a step:
+// load, weights, store, two barriers, 1750 clocks where its exponentials take
+// 1020; without the exponentials the chunk takes 255 us, with a quarter of the
+// products 273, without the copies 262.  An item's start (queries to tensor memory, the
+// first tile, and the first step twice, for its reference) costs some 10,000 clocks.  One
+// slot of 128 columns a row tile, the softmax waiting for each product, was 7%
+// slower.
 //
 // The items that would not fill a last round of the SMs (all of them, where
 // there are fewer items than SMs) have their KV tiles cut into runs, a block
