@@ -79,8 +79,9 @@ BASISKV_API int basiskv_cache4_route(const basiskv_dims* dims, const basiskv_bf1
 
 /* basiskv_attend over 4-bit caches, with the latents written as bf16 [B][Hq][r_v]
  * (fp32 accumulation, one rounding: the input of basiskv_outproj_sources with
- * n_src = 1).  Selected pages past a sequence's length contribute nothing; a
- * group without a live selected token gets zeros. */
+ * n_src = 1).  Selected pages past a sequence's length contribute nothing, a page
+ * selected twice counts twice; a group without a live selected token gets
+ * zeros. */
 BASISKV_API int basiskv_cache4_attend(const basiskv_dims* dims, const basiskv_bf16* q,
                                       const int32_t* seq_lens, int max_seq_len,
                                       const int32_t* block_table, const uint8_t* K4,

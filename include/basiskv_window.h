@@ -14,7 +14,9 @@ extern "C" {
 
 /* Bytes of workspace basiskv_attend_window needs for n_q query tokens per
  * sequence, contexts of at most max_seq_len tokens and this mask; 0 when the
- * arguments are invalid. */
+ * arguments are invalid.  It holds for a call with these arguments, whatever the
+ * lengths: the work is split otherwise for other ones, and a smaller
+ * max_seq_len may need more. */
 BASISKV_API size_t basiskv_window_workspace_size(const basiskv_dims* dims, int n_q,
                                                  int max_seq_len, int sink_tokens, int window);
 

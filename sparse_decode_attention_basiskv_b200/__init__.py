@@ -140,6 +140,24 @@ def _stream(stream) -> int | None:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _here(stream, *tensors) -> list:
+    """Addresses of tensors (or None) that must lie on the current device,
+    where the call's kernels run, and the stream's handle behind them."""
+    import torch
+    device = torch.cuda.current_device()
+    at = []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+        elif t.get_device() != device:
+            raise ValueError(f"tensor of shape {tuple(t.shape)} is on {t.device}, the current "
+                             f"device is cuda:{device}")
+        else:
+            at.append(t.data_ptr() if t.is_contiguous() else _ptr(t))
+    at.append(torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
+    return at
+
+
 def _check(status: int, where: str) -> None:
     if status != OK:
         raise BasisKVError(status, where)
@@ -246,38 +264,39 @@ def basiskv_cache4_write(dims: Dims, k_new, z_new, e_new, n_new: int, seq_lens, 
     """Rounds rows of k, z and e (e_new and E4 may be None) to 4 bits into
     their pages behind seq_lens; lens_out (seq_lens itself, another buffer or
     None) receives the lengths after it."""
+    k, z, e, *rest = _here(stream, k_new, z_new, e_new, seq_lens, lens_out, block_table,
+                          K4, Z4, E4)
     _check(load_library().basiskv_cache4_write(
-        ctypes.byref(dims), _ptr(k_new), _ptr(z_new), _ptr(e_new), n_new, _ptr(seq_lens),
-        _ptr(lens_out), _ptr(block_table), _ptr(K4), _ptr(Z4), _ptr(E4), _stream(stream)),
-        "basiskv_cache4_write")
+        ctypes.byref(dims), k, z, e, n_new, *rest), "basiskv_cache4_write")
 
 
 def basiskv_cache4_read(dims: Dims, first, count: int, seq_lens, block_table, K4, Z4, E4, k_out,
                         z_out, e_out, stream=None) -> None:
     """Reads tokens first[b] .. first[b] + count - 1 back as bf16 values (a
     cache and its output may be None together)."""
+    start, *rest = _here(stream, first, seq_lens, block_table, K4, Z4, E4, k_out, z_out, e_out)
     _check(load_library().basiskv_cache4_read(
-        ctypes.byref(dims), _ptr(first), count, _ptr(seq_lens), _ptr(block_table), _ptr(K4),
-        _ptr(Z4), _ptr(E4), _ptr(k_out), _ptr(z_out), _ptr(e_out), _stream(stream)),
-        "basiskv_cache4_read")
+        ctypes.byref(dims), start, count, *rest), "basiskv_cache4_read")
 
 
 def basiskv_cache4_route(dims: Dims, q, seq_lens, max_seq_len: int, block_table, P_K, U_K, Z4,
                          E4, top_k: int, page_scores, sel, workspace, stream=None) -> None:
     """basiskv_route over 4-bit caches."""
+    q, lens, table, pk, uk, z, e, scores, sel, ws, st = _here(
+        stream, q, seq_lens, block_table, P_K, U_K, Z4, E4, page_scores, sel, workspace)
     _check(load_library().basiskv_cache4_route(
-        ctypes.byref(dims), _ptr(q), _ptr(seq_lens), max_seq_len, _ptr(block_table),
-        _ptr(P_K), _ptr(U_K), _ptr(Z4), _ptr(E4), top_k, _ptr(page_scores), _ptr(sel),
-        _ptr(workspace), _nbytes(workspace), _stream(stream)), "basiskv_cache4_route")
+        ctypes.byref(dims), q, lens, max_seq_len, table, pk, uk, z, e, top_k, scores, sel, ws,
+        _nbytes(workspace), st), "basiskv_cache4_route")
 
 
 def basiskv_cache4_attend(dims: Dims, q, seq_lens, max_seq_len: int, block_table, K4, Z4, sel,
                           top_k: int, a_out, workspace, stream=None) -> None:
     """basiskv_attend over 4-bit caches; a_out bf16 [B][Hq][r_v]."""
+    q, lens, table, k, z, sel, out, ws, st = _here(stream, q, seq_lens, block_table, K4, Z4, sel,
+                                                   a_out, workspace)
     _check(load_library().basiskv_cache4_attend(
-        ctypes.byref(dims), _ptr(q), _ptr(seq_lens), max_seq_len, _ptr(block_table), _ptr(K4),
-        _ptr(Z4), _ptr(sel), top_k, _ptr(a_out), _ptr(workspace), _nbytes(workspace),
-        _stream(stream)), "basiskv_cache4_attend")
+        ctypes.byref(dims), q, lens, max_seq_len, table, k, z, sel, top_k, out, ws,
+        _nbytes(workspace), st), "basiskv_cache4_attend")
 
 
 def window_workspace_size(dims: Dims, n_q: int, max_seq_len: int, sink_tokens: int,
@@ -294,10 +313,11 @@ def basiskv_attend_window(dims: Dims, q, n_q: int, seq_lens, max_seq_len: int, b
     window (0: everything) and the first sink_tokens tokens; bf16 or E4M3
     caches by dims.cache_fp8, or 4-bit ones.  q bf16 [B][n_q][Hq][d], a_out
     bf16 [B][n_q][Hq][r_v]."""
+    q, lens, table, k, z, out, ws, st = _here(stream, q, seq_lens, block_table, K_cache, Z_cache,
+                                              a_out, workspace)
     _check(load_library().basiskv_attend_window(
-        ctypes.byref(dims), _ptr(q), n_q, _ptr(seq_lens), max_seq_len, _ptr(block_table),
-        _ptr(K_cache), _ptr(Z_cache), int(cache4), sink_tokens, window, _ptr(a_out),
-        _ptr(workspace), _nbytes(workspace), _stream(stream)), "basiskv_attend_window")
+        ctypes.byref(dims), q, n_q, lens, max_seq_len, table, k, z, int(cache4), sink_tokens,
+        window, out, ws, _nbytes(workspace), st), "basiskv_attend_window")
 
 
 def read_device_status(stream=None) -> int:

@@ -213,3 +213,29 @@ def test_mix_equals_a_plain_softmax():
     np.testing.assert_allclose(a[2], w @ Z / w.sum(), rtol=1e-12)
     w = np.exp(K[:2] @ q[0] / np.sqrt(8))
     np.testing.assert_allclose(a[0], w @ Z[:2] / w.sum(), rtol=1e-12)
+
+
+def test_binding_refuses_tensors_elsewhere(monkeypatch):
+    """Tensors in host memory, or on another device than the current one, never
+    reach the library."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(bkv, "load_library", lambda *a: pytest.fail("the library was called"))
+    monkeypatch.setattr(bkv, "_lib", None)
+    t, d = torch.zeros(4), _dims()
+    for call in (
+            lambda: bkv.basiskv_cache4_write(d, t, t, t, 1, t, t, t, t, t, t),
+            lambda: bkv.basiskv_cache4_write(d, t, t, None, 1, t, None, t, t, t, None),
+            lambda: bkv.basiskv_cache4_read(d, t, 1, t, t, t, t, t, t, t, t),
+            lambda: bkv.basiskv_cache4_route(d, t, t, 9, t, t, t, t, t, 2, t, t, t),
+            lambda: bkv.basiskv_cache4_attend(d, t, t, 9, t, t, t, t, 2, t, t),
+            lambda: bkv.basiskv_attend_window(d, t, 1, t, 9, t, t, t, 0, 0, t, t)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+    class Elsewhere:  # a tensor of a second GPU
+        shape, device = (4,), "cuda:1"
+        get_device = staticmethod(lambda: 1)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        bkv._here(None, None, Elsewhere())

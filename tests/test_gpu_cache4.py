@@ -281,6 +281,24 @@ def test_selected_attention(B, G, Hkv, d, rv, rk, page, lens, top_k, scale):
     assert torch.equal(out, first)
 
 
+def test_a_page_selected_twice_counts_twice():
+    G, Hkv, d, rv, page, L = 4, 2, 128, 64, 16, 100
+    rng, dims, table, K, Z, E, q, *_ = _cache_problem(12, 1, G, Hkv, d, rv, 32, page, [L])
+    sel = np.array([[[0, 3, 3, 6], [6, -1, 6, 6]]], dtype=np.int32)
+    out = torch.zeros(1, G * Hkv, rv, dtype=torch.bfloat16, device="cuda")
+    bkv.basiskv_cache4_attend(dims, q.cuda(), torch.tensor([L], dtype=torch.int32, device="cuda"),
+                              L, torch.from_numpy(table).cuda(), K.tensor, Z.tensor,
+                              torch.from_numpy(sel).cuda(), 4, out, _workspace(dims, 4, L))
+    status_clean()
+    for g in range(Hkv):
+        t = np.concatenate([np.arange(p * page, min((p + 1) * page, L)) for p in sel[0, g]
+                            if p >= 0])
+        a, A, X = reference(q[0, g * G:(g + 1) * G].double().numpy(), K.values[0][t][:, g],
+                            Z.values[0][t][:, g], np.ones((G, len(t)), dtype=bool))
+        assert_rows(out[0, g * G:(g + 1) * G].cpu().double().numpy(), a, A, X,
+                    FMT_WEIGHT["4bit"], f"g{g}")
+
+
 def test_selected_attention_reports_bad_pages():
     B, G, Hkv, d, rv, rk, page, lens = 1, 4, 2, 128, 64, 32, 16, [100]
     rng, dims, table, K, Z, E, q, *_ = _cache_problem(10, B, G, Hkv, d, rv, rk, page, lens)
