@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
   int k_next = 2 * NB;
   int slot = 0;
   uint32_t phase = 0;
+  bool landing = true;  // no wait has run out yet (the others would, too)
 
   for (int seg = 0; seg < run;) {
     int b, g, u0, item_end;
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
         }
     }
     for (; seg < item_end; ++seg, ++u0) {
-      mbar_poll(bars + warp * NST + slot, phase, a.status);
+      landing = landing && mbar_poll(bars + warp * NST + slot, phase, a.status);
       const uint2 tag = tags[warp][slot];
       const uint32_t st = ring + slot * UB;
       const int t0 = u0 * kR4Unit;

@@ -378,6 +378,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) request();
   int slot = 0;
+  bool landing = true;  // no wait has run out yet (the others would, too)
   uint32_t phase = 0;  // of the slots' barriers in this turn of the ring
 
   // 4-bit units: byte offsets of half 1's codes and of the halves' scales
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
       __syncwarp();  // every lane is done with the slot that is filled next
       request();
       if constexpr (BULK) {
-        mbar_poll(bars + warp * NST + slot, phase, a.status);
+        landing = landing && mbar_poll(bars + warp * NST + slot, phase, a.status);
       } else {
         cp_async_wait_group<NST - 1>();
         __syncwarp();
