@@ -20,11 +20,11 @@
 // significant bits; each head is first scaled by a power of two that puts its
 // largest magnitude into [2^14, 2^15), divided out of the scores again).
 //
-// Measured: 16 x 32K tokens, 8 KV heads, r_v 64, r_k 32 (228 MB): 63 us with the
-// folding of the queries and the choice of pages, 3.6 TB/s; the instructions of the widening
-// bound it (about 13 a 32-token unit and column pair of a lane).  A ring a
+// Measured: 16 x 32K tokens, 8 KV heads, r_v 64, r_k 32 (228 MB): 64 us with the
+// folding of the queries and the choice of pages, 3.6 TB/s; the widening's
+// instructions bound it (68% of the issue slots).  A ring a
 // warp with one unit requested at a time took 70 us, a fourth of the warps as
-// loaders for the others 101 us, two CTAs an SM instead of three 64 us.
+// loaders for the others 101 us, two CTAs an SM instead of three 65 us.
 #include "cache4.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
   constexpr int PP = ONE ? 1 : 2;  // pages a unit
   extern __shared__ __align__(128) uint8_t r4_smem[];
   __shared__ long long pre[257];
+  __shared__ int lens[kLineMaxSeqs];
   __shared__ uint64_t bars[kR4Warps * NST];
   __shared__ uint2 tags[kR4Warps][NST];  // the unit's pages: 1 there, 0 missing
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, c = lane & 3;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
     return len >= 0 && len <= a.max_seq_len ? (len + kR4Unit - 1) / kR4Unit : 0;
   };
   line_scan(a.B, pre, [&](int b) -> long long {
-    const int len = a.seq_lens[b];
+    const int len = lens[b] = a.seq_lens[b];
     if (blockIdx.x == 0 && (len < 0 || len > a.max_seq_len))
       raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
     return units_of(len);
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
     const unsigned y = (unsigned)(x - pre[b] * a.Hkv);  // below Hkv * U
     id_g = (int)(y / (unsigned)U);
     const int p = (int)(y - (unsigned)id_g * U) * PP;
-    const int P = (a.seq_lens[b] + a.S - 1) / a.S;
+    const int P = (lens[b] + a.S - 1) / a.S;
     auto look = [&](int q) {
       int id = q < P ? __ldg(a.block_table + (size_t)b * a.max_pages + q) : -1;
       if (q < P && (id < 0 || id >= a.num_phys)) {
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
       u0 = (int)(y - (unsigned)g * U);
       item_end = min(run, seg + U - u0);
     }
-    const int T = a.seq_lens[b];
+    const int T = lens[b];
     float* out = a.scores + ((size_t)b * a.Hkv + g) * a.max_pages;
     // ---- folded queries: column n of group j is head 4 j + n / 2, part n % 2
     uint32_t qb[KS][NJ][2];

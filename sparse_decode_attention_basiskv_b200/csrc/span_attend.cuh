@@ -45,8 +45,8 @@
 // significant bits, a second product) where they are bf16.
 //
 // Measured (16 x 32K tokens, 8 KV heads, d 128, r_v 64, G 4): bf16, window 4096
-// (202 MB) 42 us, 4.8 TB/s; 4 bits, all tokens (453 MB) 112 us, 4.0 TB/s, half of it
-// the widening's issue slots (1 in 2.4 of them a product or a conversion); 128 selected
+// (202 MB) 42 us, 4.8 TB/s; 4 bits, all tokens (453 MB) 114 us, 4.0 TB/s, bound
+// by issue slots (62% used) and the conversions' pipe; 128 selected
 // pages of 4 bits (28 MB) 19 us, a start of 8 us and one turn of the ring;
 // E4M3, 7 ragged sequences, window 8192, 20 rows (89 MB) 43 us against 69 on
 // the prompt kernel.  Joining the partials of an item with one CTA took 23 us
@@ -109,11 +109,14 @@ __device__ __forceinline__ SpanSeq span_seq(const SpanArgs& a, int len) {
   return s;
 }
 
-// pre[b] = units of one KV head of the sequences before b; pre[B] = all.
+// pre[b] = units of one KV head of the sequences before b; pre[B] = all.  The
+// lengths are left in lens for the lookups that follow, where that is given.
 template <int UT>
-__device__ __forceinline__ void span_scan(const SpanArgs& a, long long* pre, bool report) {
+__device__ __forceinline__ void span_scan(const SpanArgs& a, long long* pre, bool report,
+                                          int* lens = nullptr) {
   line_scan(a.B, pre, [&](int b) -> long long {
     const int len = a.seq_lens[b];
+    if (lens) lens[b] = len;
     if (report && (len < 0 || len > a.max_seq_len)) raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
     return span_seq<UT>(a, len).n;
   });
@@ -197,6 +200,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
   static_assert(NST >= 2 && (D + RV) * UT / 16 * 9 % 16 == 0, "");
   extern __shared__ __align__(128) uint8_t sp_smem_raw[];
   __shared__ long long pre[257];
+  __shared__ int lens[kLineMaxSeqs];
   __shared__ uint2 tags[kSpWarps][NST];      // a unit's halves: first tokens (~0: absent)
   __shared__ uint64_t bars[kSpWarps * NST];  // a unit has landed
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = lane >> 2, c = lane & 3;
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
   if (BULK) fence_barrier_init();
   pdl_wait();
   pdl_launch_dependents();
-  span_scan<UT>(a, pre, blockIdx.x == 0);
+  span_scan<UT>(a, pre, blockIdx.x == 0, lens);
   const long long total = pre[a.B] * a.Hkv;
   const int C = span_ctas(total, gridDim.x);
   if ((int)blockIdx.x >= C) return;
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
     if (k >= n_units) return;
     const long long x = start + warp + (long long)kSpWarps * k;
     const int b = line_find(a.B, pre, a.Hkv, x);
-    const SpanSeq sq = span_seq<UT>(a, a.seq_lens[b]);
+    const SpanSeq sq = span_seq<UT>(a, lens[b]);
     const long long y = x - pre[b] * a.Hkv;
     const int g = (int)(y / sq.n), u = (int)(y - (long long)g * sq.n);
     const int lo = a.window > 0 ? max(0, max(sq.T - a.n_tot, 0) - a.window + 1) : 0;
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
     {
       const long long x = start + seg;
       b = line_find(a.B, pre, a.Hkv, x);
-      sq = span_seq<UT>(a, a.seq_lens[b]);
+      sq = span_seq<UT>(a, lens[b]);
       const long long y = x - pre[b] * a.Hkv;
       g = (int)(y / sq.n);
       const int u = (int)(y - (long long)g * sq.n);  // the item's unit at seg
