@@ -21,9 +21,8 @@
 // largest magnitude into [2^14, 2^15), divided out of the scores again).
 //
 // Measured: 16 x 32K tokens, 8 KV heads, r_v 64, r_k 32 (228 MB): 64 us with the
-// folding of the queries and the choice of pages, 3.6 TB/s; the widening's
-// instructions bound it (68% of the issue slots).  A ring a
-// warp with one unit requested at a time took 70 us, a fourth of the warps as
+// folding of the queries, 3.6 TB/s; the widening's instructions bound it (68% of
+// the issue slots).  Rings with one unit requested at a time took 70 us, a fourth of the warps as
 // loaders for the others 101 us, two CTAs an SM instead of three 65 us.
 #include "cache4.cuh"
 #include "common.cuh"
