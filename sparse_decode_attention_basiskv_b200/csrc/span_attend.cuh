@@ -48,7 +48,7 @@
 // (202 MB) 42 us, 4.8 TB/s; 4 bits, all tokens (453 MB) 114 us, 4.0 TB/s, bound
 // by issue slots (62% used) and the conversions' pipe; 128 selected
 // pages of 4 bits (28 MB) 19 us, a start of 8 us and one turn of the ring;
-// E4M3, 7 ragged sequences, window 8192, 20 rows (89 MB) 43 us against 69 on
+// E4M3, 7 ragged sequences, window 8192, 20 rows (89 MB) 41 us against 69 on
 // the prompt kernel.  Joining the partials of an item with one CTA took 23 us
 // longer there; one output a thread, over more CTAs, about 2.
 //
@@ -120,6 +120,11 @@ __device__ __forceinline__ void span_scan(const SpanArgs& a, long long* pre, boo
     if (report && (len < 0 || len > a.max_seq_len)) raise_status(a.status, BASISKV_DEV_BAD_LENGTH);
     return span_seq<UT>(a, len).n;
   });
+}
+
+// x / n for line positions, which seldom need 64 bits.
+__device__ __forceinline__ long long line_div(long long x, int n) {
+  return (unsigned long long)x >> 32 ? x / n : (long long)((unsigned)x / (unsigned)n);
 }
 
 // CTAs that share the line: all of the grid, or fewer when the lengths at hand
@@ -222,8 +227,8 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
   __shared__ long long start;
   int run;
   {
-    const long long s0 = total * blockIdx.x / C;
-    run = (int)(total * (blockIdx.x + 1) / C - s0);
+    const long long s0 = line_div(total * blockIdx.x, C);
+    run = (int)(line_div(total * (blockIdx.x + 1), C) - s0);
     if (tid == 0) start = s0;
   }
   __syncthreads();
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
     const int b = line_find(a.B, pre, a.Hkv, x);
     const SpanSeq sq = span_seq<UT>(a, lens[b]);
     const long long y = x - pre[b] * a.Hkv;
-    const int g = (int)(y / sq.n), u = (int)(y - (long long)g * sq.n);
+    const int g = (int)line_div(y, sq.n), u = (int)(y - (long long)g * sq.n);
     const int lo = a.window > 0 ? max(0, max(sq.T - a.n_tot, 0) - a.window + 1) : 0;
     auto tile_row = [&](int t) -> int {
       // no row sees tokens between the sinks and the window: their pages are
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
       b = line_find(a.B, pre, a.Hkv, x);
       sq = span_seq<UT>(a, lens[b]);
       const long long y = x - pre[b] * a.Hkv;
-      g = (int)(y / sq.n);
+      g = (int)line_div(y, sq.n);
       const int u = (int)(y - (long long)g * sq.n);  // the item's unit at seg
       item_end = min(run, seg + sq.n - u);
       alone = u == 0 && item_end == seg + sq.n;
@@ -419,42 +424,48 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
     // of rows 2c, 2c + 1 (+ 8), whose scores the lane gets: score factor, position
     float sl[NR][2];
     int pos[NR][2];
+    auto column = [&](int k, int e) {  // of the pair in qb[k][.][e]
+      return FMT == kSpanBf16 ? 16 * k + 8 * e + 2 * c
+             : FMT == kSpanE4m3 ? 64 * (k >> 2) + 16 * c + 4 * (k & 3) + 2 * e
+                                : (D / 4) * c + 4 * k + 2 * e;
+    };
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int r = n + 8 * i;
-      const int j = r / a.G, h = r - j * a.G;
+    for (int i = 0; i < NR; ++i) {  // all loads before the first use
+      const int r = n + 8 * i, j = r >> a.logG, h = r & (a.G - 1);
       const bool ok = r < R;
       const uint16_t* qr =
           a.q + (((size_t)b * a.n_tot + (ok ? j : 0)) * a.Hq + g * a.G + (ok ? h : 0)) * D;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 8 * i + 2 * c + e;
-        pos[i][e] = row < R ? pos0 + row / a.G : -1;
-        sl[i][e] = a.scale_log2;
-      }
-      if constexpr (FMT == kSpanBf16) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < KS; ++k) {
+        if constexpr (FMT == kSpanBf16) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            qb[k][i][e] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 * e + 2 * c))
-                             : 0u;
-      } else {
-        // k-step k of the lane's columns: 4 consecutive ones (2 pairs)
-        float mq = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const int col = FMT == kSpanE4m3 ? 64 * (k >> 2) + 16 * c + 4 * (k & 3)
-                                           : (D / 4) * c + 4 * k;
-          const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(qr + col)) : make_uint2(0u, 0u);
+            qb[k][i][e] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qr + column(k, e))) : 0u;
+        } else {
+          const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(qr + column(k, 0)))
+                             : make_uint2(0u, 0u);
           qb[k][i][0] = w.x;
           qb[k][i][1] = w.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * i + 2 * c + e;
+        pos[i][e] = row < R ? pos0 + (row >> a.logG) : -1;
+        sl[i][e] = a.scale_log2;
+      }
+      if constexpr (FMT != kSpanBf16) {
+        float mq = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 f = bf16x2_to_f2(qb[k][i][e]);
             mq = fmaxf(mq, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
-        }
         mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
         mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
         const int ex = mq > 0.f ? (int)((__float_as_uint(mq) >> 23) & 0xffu) - 126 : 15;
@@ -855,7 +866,7 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
         }
         if (alone) {
           const float L = meet[(size_t)rr * RS + RV + 3], inv = L > 0.f ? 1.f / L : 0.f;
-          const int j = r / a.G, h = r - j * a.G;
+          const int j = r >> a.logG, h = r & (a.G - 1);
           uint16_t* dst = a.out + (((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV;
           const float v[4] = {A.x * inv, A.y * inv, A.z * inv, A.w * inv};
 #pragma unroll
@@ -906,7 +917,7 @@ __global__ void __launch_bounds__(kSpThreads) span_merge_kernel(SpanArgs a, int 
     A = fmaf(A, f0, ac * f1);
     M = mn;
   }
-  const int j = r / a.G, h = r - j * a.G, col = sp_col<FMT, RV>(at >> 3, at & 7);
+  const int j = r >> a.logG, h = r & (a.G - 1), col = sp_col<FMT, RV>(at >> 3, at & 7);
   a.out[(((size_t)b * a.n_tot + j) * a.Hq + g * a.G + h) * RV + col] =
       f_to_bf16(L > 0.f ? A / L : 0.f);
 }
