@@ -45,10 +45,19 @@
 // slot of 128 columns a row tile, the softmax waiting for each product, was 7%
 // slower.
 //
+// Tokens whose block-table entry is out of range have no part in the softmax: the
+// issuing warp, which looks the run's entries up at the start, sets their scores to
+// -infinity in tensor memory behind Q K^T.  A run with such an entry takes a loop
+// of its own.  (Tests in the softmax, whose registers are full, took 7 to 11% of
+// every call, one in the issuing warps' common loop up to 7%; this way the calls
+// without such entries take -2 to +3%.)
+//
 // The items that would not fill a last round of the SMs (all of them, where
 // there are fewer items than SMs) have their KV tiles cut into runs, a block
 // each, whose partial sums span_tc_merge_kernel joins.
 #pragma once
+
+#include <type_traits>
 
 #include "cache4.cuh"
 #include "common.cuh"
@@ -82,6 +91,8 @@ struct TcGeom {
   // its columns: S of row tile t at 128 t, then O, then Q
   static constexpr int kO = 256, kQ = kO + 2 * RV;
   static_assert(kQ + 16 * kQSteps <= 512, "");
+  // (d 128, r_v 128: 12 KB more left the rows that the loaders widen half the L1, and
+  // took an E4M3 chunk from 417 to 484 us)
   static constexpr size_t kSmem = 1024 + kQBytes + kStages * (size_t)(kKBytes + kZBytes);
 };
 
@@ -177,7 +188,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
   constexpr bool BF = FMT == kSpanBf16;
   extern __shared__ uint8_t tc_smem_raw[];
   uint8_t* smem = align_smem_1k(tc_smem_raw);
-  __shared__ uint64_t bars[4 * NST + 9];
+  __shared__ uint64_t bars[4 * NST + 11];
+  __shared__ __align__(128) uint32_t no_score[128];  // -infinity, 32 rows of 4 columns
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float row_scale[kTcRows];
@@ -185,6 +197,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
   // [row tile][slot]: S of step u is there and O has step u - 2 (two phases more
   // than there are steps); P is there
   uint64_t *sfull = bars + 4 * NST, *pfull = sfull + 4, *qfull = sfull + 8;
+  uint64_t* scored = qfull + 1;  // [row tile]: Q K^T of a step with missing tokens is done
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const uint32_t sq = smem_u32(smem), sk = sq + Gm::kQBytes, sz = sk + NST * Gm::kKBytes;
@@ -208,6 +221,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
       mbar_init(&pfull[t], 4);
     }
     mbar_init(qfull, 8);
+    mbar_init(&scored[0], 1);
+    mbar_init(&scored[1], 1);
     abort_flag = 0;
     fence_barrier_init();
   }
@@ -217,6 +232,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
                  "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == 2) {
+    sts128(smem_u32(no_score + 4 * lane), 0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+    fence_proxy_async();
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -245,6 +263,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int* abrt = &abort_flag;
+  // The block-table entry of logical page p, or -1 where it is out of range.
+  auto entry = [&](int p) {
+    const int pp = p < a.max_pages ? __ldg(a.block_table + (size_t)it.b * a.max_pages + p) : -1;
+    return pp < a.num_phys ? pp : -1;
+  };
   // steps of 64 tokens; the last tile's second half may be past every row
   const int n2 = n == 0 ? 0
                         : 2 * n - (i0 + n == it.n && ((it.live_end - 1) & 127) < 64 ? 1 : 0);
@@ -263,59 +286,96 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
       auto wait = [&](uint64_t* bar, int parity) {
         return mbar_poll(bar, parity, a.status, abrt);
       };
-      // step u of KV tile u / 2 in ring stage st: rows 64 (u % 2) .. of the tile
-      auto qk = [&](int u, int st) {
-        tc_fence_after_sync();
-        if (lead) {
-          const uint64_t k0 = dk + st * (Gm::kKBytes >> 4) + (u & 1) * (64 * 128 >> 4);
+      // is the page of a token among t .. t + count - 1 (of one page) needed and not there?
+      auto missing = [&](int t, int count) {
+        return t < it.live_end && (t + count > it.lo_first || t < a.sink) &&
+               entry(t >> a.logS) < 0;
+      };
+      bool gap = false;  // (looked up while the first tile is on its way)
+      const int lp = 7 - a.logS;  // log2 of a tile's pages
+      for (int x = lane; x < n << lp; x += 32)
+        gap |= missing((tc_tile(it, i0 + (x >> lp)) * 128) + ((x & ((1 << lp) - 1)) << a.logS), a.S);
+      gap = __any_sync(0xffffffffu, gap);
+      int scored_ph = 0;
+      auto issue = [&](auto gaps) {
+        constexpr bool GAPS = decltype(gaps)::value;
+        // step u of KV tile u / 2 in ring stage st: rows 64 (u % 2) .. of the tile
+        auto qk = [&](int u, int st) -> bool {
+          bool ok = true;
+          tc_fence_after_sync();
+          if (lead) {
+            const uint64_t k0 = dk + st * (Gm::kKBytes >> 4) + (u & 1) * (64 * 128 >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t kk = k0 + (k >> 2) * 1024 + (k & 3) * 2;
-            if (k < Gm::kQSteps)
-              tc_mma_ts(tm_s + 64 * (u & 1), tm_q + 8 * k, kk, id_qk, k > 0);
-            else
-              tc_mma_ss(tm_s + 64 * (u & 1), dq + (k >> 2) * 1024 + (k & 3) * 2, kk, id_qk, k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t kk = k0 + (k >> 2) * 1024 + (k & 3) * 2;
+              if (k < Gm::kQSteps)
+                tc_mma_ts(tm_s + 64 * (u & 1), tm_q + 8 * k, kk, id_qk, k > 0);
+              else
+                tc_mma_ss(tm_s + 64 * (u & 1), dq + (k >> 2) * 1024 + (k & 3) * 2, kk, id_qk, k > 0);
+            }
           }
-          tc_commit_to(&sfull[2 * t + (u & 1)]);
-          if (u & 1) tc_commit_to(&kempty[st]);
+          if constexpr (GAPS) {
+            // 8 tokens a lane: they lie in one page
+            const int t8 = tc_tile(it, i0 + (u >> 1)) * 128 + 64 * (u & 1) + 8 * (lane & 7);
+            const uint32_t miss = __ballot_sync(0xffffffffu, lane < 8 && missing(t8, 8));
+            if (miss) {
+              if (lead) tc_commit_to(&scored[t]);
+              ok = wait(&scored[t], scored_ph);
+              scored_ph ^= 1;
+              tc_fence_after_sync();
+              if (lead && ok) {
+                for (int c = 0; c < 16; ++c)
+                  if (miss >> (c >> 1) & 1)
+                    tc_cp_32x4(tm_s + 64 * (u & 1) + 4 * c, tc_sdesc_plain(smem_u32(no_score)));
+              }
+            }
+          }
+          if (lead) {
+            tc_commit_to(&sfull[2 * t + (u & 1)]);
+            if (u & 1) tc_commit_to(&kempty[st]);
+          }
+          __syncwarp();
+          return ok;
+        };
+        int kst = 0, kph = 0, zst = 0, zph = 0;  // stages of the next Key and latent tiles
+        auto next = [](int& st, int& ph) {
+          if (++st == NST) {
+            st = 0;
+            ph ^= 1;
+          }
+        };
+        bool ok = wait(qfull, 0) && wait(&kfull[0], 0);
+        if (ok) {
+          ok = qk(0, 0) && (n2 == 1 || qk(1, 0));
+          next(kst, kph);
         }
-        __syncwarp();
-      };
-      int kst = 0, kph = 0, zst = 0, zph = 0;  // stages of the next Key and latent tiles
-      auto next = [](int& st, int& ph) {
-        if (++st == NST) {
-          st = 0;
-          ph ^= 1;
-        }
-      };
-      bool ok = wait(qfull, 0) && wait(&kfull[0], 0);
-      if (ok) {
-        qk(0, 0);
-        if (n2 > 1) qk(1, 0);
-        next(kst, kph);
-      }
-      for (int u = 0; ok && u < n2; ++u) {
-        if (!(u & 1)) ok = wait(&zfull[zst], zph);
-        ok = ok && wait(&pfull[2 * t + (u & 1)], (u >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (lead) {
-          const uint64_t z = dz + zst * (Gm::kZBytes >> 4) + (u & 1) * (64 * 128 >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + k * 128, id_pv, u > 0 || k > 0);
-          if (u + 2 >= n2) tc_commit_to(&sfull[2 * t + (u & 1)]);
-          if (u & 1) tc_commit_to(&zempty[zst]);
-        }
-        __syncwarp();
-        if (u & 1) next(zst, zph);
-        if (u + 2 < n2) {
-          if (!(u & 1)) ok = wait(&kfull[kst], kph);
+        for (int u = 0; ok && u < n2; ++u) {
+          if (!(u & 1)) ok = wait(&zfull[zst], zph);
+          ok = ok && wait(&pfull[2 * t + (u & 1)], (u >> 1) & 1);
           if (!ok) break;
-          qk(u, kst);  // step u + 2: the next tile's half of the same parity
-          if (u & 1) next(kst, kph);
+          tc_fence_after_sync();
+          if (lead) {
+            const uint64_t z = dz + zst * (Gm::kZBytes >> 4) + (u & 1) * (64 * 128 >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + k * 128, id_pv, u > 0 || k > 0);
+            if (u + 2 >= n2) tc_commit_to(&sfull[2 * t + (u & 1)]);
+            if (u & 1) tc_commit_to(&zempty[zst]);
+          }
+          __syncwarp();
+          if (u & 1) next(zst, zph);
+          if (u + 2 < n2) {
+            if (!(u & 1)) ok = wait(&kfull[kst], kph);
+            if (!ok) break;
+            ok = qk(u + 2, kst);  // in the slot of step u
+            if (u & 1) next(kst, kph);
+          }
         }
-      }
+      };
+      if (gap)
+        issue(std::true_type{});
+      else
+        issue(std::false_type{});
     }
   } else if (warp >= 12) {
     // -------------------------------------------------------------- loaders

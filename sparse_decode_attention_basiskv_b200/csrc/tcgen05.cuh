@@ -21,6 +21,12 @@ __device__ __forceinline__ uint64_t tc_sdesc(uint32_t saddr, uint32_t lbo = 16) 
          (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// Shared-memory descriptor of 32 rows of 16 bytes, one behind the other.
+__device__ __forceinline__ uint64_t tc_sdesc_plain(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3fff) | (uint64_t)(128 >> 4) << 16 |
+         (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
 __device__ __forceinline__ void tc_fence_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
@@ -45,6 +51,11 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
+}
+// 32 rows of 16 bytes from shared memory into four tensor-memory columns of each
+// quarter of the lanes.
+__device__ __forceinline__ void tc_cp_32x4(uint32_t d, uint64_t s) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(s) : "memory");
 }
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {

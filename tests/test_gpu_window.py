@@ -264,3 +264,39 @@ def test_a_bad_page_is_left_out_of_a_tokens_softmax():
     see[:, 32:48] = False
     a, A, X = reference(p.q[0, 0].double().numpy(), p.K.values[0][:, 0], p.Z.values[0][:, 0], see)
     assert_rows(p.out[0, 0].cpu().double().numpy(), a, A, X, FMT_WEIGHT["bf16_token"])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [1, 5, 24, 200])
+@pytest.mark.parametrize("G,d,rv,page,window,sink", [(4, 64, 32, 16, 0, 0), (4, 128, 128, 32, 0, 0),
+                                                     (8, 128, 64, 16, 90, 40)])
+def test_bad_pages_are_left_out_of_the_softmax(fmt, n, G, d, rv, page, window, sink):
+    """Tokens of pages whose table entry is out of range have no part in any row's
+    softmax, by either kernel: the oracle does not see them.  Bad pages lie among the
+    sinks, in the middle, in both halves of a 128-token tile, side by side, and at the
+    end; a sequence whose every page is bad gives zeros."""
+    lens = [1000, 390, 50]
+    p = Problem(fmt, 3, G, 2, d, rv, page, lens, n, window, sink)
+    bad = [[0, 5, 6, 17, 18, 19, (1000 - 1) // page], [2, (390 - 1) // page], range(-(-50 // page))]
+    seen = [SO.window_mask(L, n, window, sink) for L in lens]
+    hit = False
+    for b, pages in enumerate(bad):
+        for x in pages:
+            live = seen[b][:, x * page:(x + 1) * page]
+            hit |= bool(live.any())
+            live[:] = False
+            p.table[b, x] = p.dims.num_phys_pages if x % 2 else -3
+    assert hit
+    p.run()
+    assert bkv.read_device_status() == bkv.DEV_BAD_PAGE
+    got = p.out.cpu().double().numpy()
+    kind = fmt if fmt != "bf16" else "bf16_token" if n * G <= 16 else "bf16_prompt"
+    for b, L in enumerate(lens):
+        see = np.repeat(seen[b], G, 0)
+        for g in range(2):
+            hs = slice(g * G, (g + 1) * G)
+            a, A, X = reference(p.q[b, :, hs].double().numpy().reshape(-1, d),
+                                p.K.values[b][:, g], p.Z.values[b][:, g], see)
+            assert_rows(got[b, :, hs].reshape(-1, rv), a, A, X, FMT_WEIGHT[kind],
+                        f"{fmt} n{n} b{b} g{g}")
+    assert np.all(got[2] == 0)
