@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(kC4Threads, kC4Warps * 32 / kC4Threads)
   int t0;  // token of row 0
   if constexpr (WRITE) {
     const bool fits = len >= 0 && (long long)len + a.n <= (long long)a.max_pages * a.S;
-    if (a.lens_out && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
       if (!fits) raise_status(a.status, BASISKV_DEV_OVERFLOW);
-      a.lens_out[b] = fits ? len + a.n : len;
+      if (a.lens_out) a.lens_out[b] = fits ? len + a.n : len;
     }
     if (!fits) return;
     t0 = len;

@@ -423,3 +423,31 @@ def test_serving_run_of_all_of_them():
             mag = np.abs(W.double().numpy()) @ np.abs(ya)
             assert np.all(np.abs(y[b].cpu().double().numpy() - ref)
                           <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * mag)
+
+
+@pytest.mark.parametrize("lens_out", ["none", "other", "in_place"])
+@pytest.mark.parametrize("bad", [28, 32, -1])
+def test_overflow_is_reported_whatever_becomes_of_the_lengths(lens_out, bad):
+    """A sequence whose rows do not fit is skipped whole and reported, and its length
+    stays, whether the lengths are advanced in place, in another buffer or not at all."""
+    rng = np.random.default_rng(4)
+    B, n, Hkv, d, rv, rk, page, mp = 3, 5, 2, 64, 32, 16, 16, 2
+    phys = B * mp
+    table = table_of(rng, B, mp, phys)
+    dims = dims_of(B, 8, Hkv, d, rv, rk, page, mp, phys)
+    k, z, e = (_dev(p) for p in _write_case(rng, B, n, Hkv, d, rv, rk, page, None, mp))
+    caches = [torch.full((bkv.cache4_bytes(dims, w),), 0x5A, dtype=torch.uint8, device="cuda")
+              for w in (d, rv, rk)]
+    lens = [0, bad, 27]
+    L = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = {"none": None, "other": torch.full_like(L, -9), "in_place": L}[lens_out]
+    bkv.basiskv_cache4_write(dims, k, z, e, n, L, out, torch.from_numpy(table).cuda(), *caches)
+    assert bkv.read_device_status() == bkv.DEV_OVERFLOW
+    if out is not None:
+        assert out.tolist() == [5, bad, 32]
+    if lens_out != "in_place":
+        assert L.tolist() == lens
+    for c in caches:
+        c = c.view(phys, -1)
+        assert torch.all(c[torch.from_numpy(table[1]).long().cuda()] == 0x5A)
+        assert not torch.all(c[int(table[0, 0])] == 0x5A)
