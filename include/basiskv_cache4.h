@@ -68,7 +68,8 @@ BASISKV_API int basiskv_cache4_read(const basiskv_dims* dims, const int32_t* fir
 
 /* basiskv_route over 4-bit caches: the same scores (of the cached values),
  * selection, outputs and errors.  A sequence whose length is outside
- * [0, max_seq_len] gets no scores (BASISKV_DEV_BAD_LENGTH). */
+ * [0, max_seq_len] is taken as empty (BASISKV_DEV_BAD_LENGTH): it gets no scores,
+ * and a selection of -1. */
 BASISKV_API int basiskv_cache4_route(const basiskv_dims* dims, const basiskv_bf16* q,
                                      const int32_t* seq_lens, int max_seq_len,
                                      const int32_t* block_table, const basiskv_bf16* P_K,

@@ -292,7 +292,7 @@ int basiskv_cache4_route(const basiskv_dims* dims, const basiskv_bf16* q, const 
   SelectArgs s{r.scores, seq_lens, sel, dims->B, dims->Hkv, dims->page_size,
                dims->max_pages_per_seq, top_k, max_seq_len, 0, block_table,
                reinterpret_cast<int32_t*>(ws + L.selp), n_sink,
-               dims->recent_pages == 0 ? 1 : dims->recent_pages, 1};
+               dims->recent_pages == 0 ? 1 : dims->recent_pages, 1, 1};
   return status_of(launch_select(s, st, pdl));
 }
 

@@ -132,6 +132,9 @@ struct SelectArgs {
   // Scores per cache page (routing pages of S tokens each, S above being
   // the routing page): 1, or page_size / route_page (sel_phys then null).
   int spp;
+  // A length above max_seq_len: 0 = taken as max_seq_len (the scoring did, too),
+  // 1 = as none (its scores were not written).
+  int long_is_empty;
 };
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t st, bool pdl);
 // The selection together with a one-token append (a.n_new == 1), whose

@@ -108,7 +108,8 @@ __device__ __forceinline__ void select_group(const SelectArgs& a, int bg, uint32
     v[u] = i < P_max - ns ? __ldcg(sc + i) : 0.f;
     t[u] = (outp && i < P_max) ? bt[i] : 0;
   }
-  T = T < 0 ? 0 : (T > a.max_seq_len ? a.max_seq_len : T);
+  if (T > a.max_seq_len) T = a.long_is_empty ? 0 : a.max_seq_len;
+  T = T < 0 ? 0 : T;
   const int P = (T + a.S - 1) / a.S;
   if (a.top_k >= P) {
     for (int i = tid; i < a.top_k; i += NT) {

@@ -451,3 +451,38 @@ def test_overflow_is_reported_whatever_becomes_of_the_lengths(lens_out, bad):
         c = c.view(phys, -1)
         assert torch.all(c[torch.from_numpy(table[1]).long().cuda()] == 0x5A)
         assert not torch.all(c[int(table[0, 0])] == 0x5A)
+
+
+@pytest.mark.parametrize("long", [101, 130, 2 ** 31 - 1])
+def test_selection_of_a_bad_length_is_empty(long):
+    """A length outside [0, max_seq_len] gets no scores, and so no selection: never one
+    of what lay in the workspace or in the caller's scores."""
+    B, G, Hkv, d, rv, rk, page, lens = 3, 4, 2, 128, 64, 32, 16, [100, 90, 64]
+    rng, dims, table, K, Z, E, q, P_K, U_K = _cache_problem(8, B, G, Hkv, d, rv, rk, page, lens,
+                                                            spare=3)
+    top_k, msl = 3, 100
+    tab = torch.from_numpy(table).cuda()
+
+    def run(L, fill, own_scores):
+        ws = torch.full((bkv.workspace_size(dims, top_k, msl),), fill, dtype=torch.uint8,
+                        device="cuda")
+        scores = None
+        if own_scores:
+            scores = torch.randn(B, Hkv, table.shape[1], device="cuda") * 100
+        sel = torch.full((B, Hkv, top_k), -9, dtype=torch.int32, device="cuda")
+        bkv.basiskv_cache4_route(dims, q.cuda(), torch.tensor(L, dtype=torch.int32, device="cuda"),
+                                 msl, tab, P_K.cuda(), U_K.cuda(), Z.tensor, E.tensor, top_k,
+                                 scores, sel, ws)
+        return bkv.read_device_status(), sel.cpu()
+
+    st, good = run(lens, 0, False)
+    assert st == 0 and torch.all(good >= 0)
+    for fill, own_scores in ((0, False), (0x7F, False), (0x3C, False), (0, True)):
+        for L in ([long, 90, 64], [100, long, -1]):
+            st, sel = run(L, fill, own_scores)
+            assert st == bkv.DEV_BAD_LENGTH
+            for b in range(B):
+                if 0 <= L[b] <= msl:
+                    assert torch.equal(sel[b], good[b])
+                else:
+                    assert torch.all(sel[b] == -1)
