@@ -82,7 +82,8 @@ BASISKV_API int basiskv_cache4_route(const basiskv_dims* dims, const basiskv_bf1
  * (fp32 accumulation, one rounding: the input of basiskv_outproj_sources with
  * n_src = 1).  Selected pages past a sequence's length contribute nothing, a page
  * selected twice counts twice; a group without a live selected token gets
- * zeros. */
+ * zeros.  A sequence whose length is outside [0, max_seq_len] is taken as empty
+ * (BASISKV_DEV_BAD_LENGTH); basiskv_attend does not check it. */
 BASISKV_API int basiskv_cache4_attend(const basiskv_dims* dims, const basiskv_bf16* q,
                                       const int32_t* seq_lens, int max_seq_len,
                                       const int32_t* block_table, const uint8_t* K4,

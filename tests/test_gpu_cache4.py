@@ -486,3 +486,28 @@ def test_selection_of_a_bad_length_is_empty(long):
                     assert torch.equal(sel[b], good[b])
                 else:
                     assert torch.all(sel[b] == -1)
+
+
+def test_selected_attention_of_a_bad_length_is_zero():
+    """A sequence whose length is outside [0, max_seq_len] is taken as empty."""
+    B, G, Hkv, d, rv, rk, page, lens = 3, 4, 2, 128, 64, 32, 16, [100, 90, 64]
+    rng, dims, table, K, Z, E, q, *_ = _cache_problem(11, B, G, Hkv, d, rv, rk, page, lens)
+    ws = _workspace(dims, 3, 100)
+    out = torch.zeros(B, G * Hkv, rv, dtype=torch.bfloat16, device="cuda")
+    sel = torch.tensor([[[0, 3, -1], [1, 2, 3]]] * B, dtype=torch.int32, device="cuda")
+
+    def run(L):
+        out.fill_(7.0)
+        bkv.basiskv_cache4_attend(dims, q.cuda(), torch.tensor(L, dtype=torch.int32,
+                                                               device="cuda"), 100,
+                                  torch.from_numpy(table).cuda(), K.tensor, Z.tensor, sel, 3, out,
+                                  ws)
+        return bkv.read_device_status(), out.clone()
+
+    st, good = run(lens)
+    assert st == 0
+    for L in ([101, 90, 64], [100, -1, 2 ** 31 - 1]):
+        st, got = run(L)
+        assert st == bkv.DEV_BAD_LENGTH
+        for b in range(B):
+            assert torch.equal(got[b], good[b]) if 0 <= L[b] <= 100 else torch.all(got[b] == 0)
