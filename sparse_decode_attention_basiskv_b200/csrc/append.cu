@@ -66,7 +66,7 @@ __global__ void bump_lengths_kernel(const int32_t* seq_lens, int32_t* out, int B
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= B) return;
   const int len = seq_lens[b];
-  if (len < 0 || len + n_new > cap) {
+  if (len < 0 || len > cap - n_new) {  // (the sum may pass 32 bits)
     raise_status(status, BASISKV_DEV_OVERFLOW);
     return;
   }

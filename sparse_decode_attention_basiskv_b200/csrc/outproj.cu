@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kOpThreads, 1)
     pdl_wait();
     for (int b = lane; b < a.B; b += 32) {
       const int len = a.bump_lens[b];
-      if (len >= 0 && len + a.bump_n <= a.bump_cap) a.bump_lens[b] = len + a.bump_n;
+      if (len >= 0 && len <= a.bump_cap - a.bump_n) a.bump_lens[b] = len + a.bump_n;
     }
   }
 

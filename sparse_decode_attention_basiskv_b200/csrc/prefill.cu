@@ -190,7 +190,7 @@ __device__ __forceinline__ RowRef row_ref(const AppendArgs& a, const int* lens, 
   if (r >= rows) return x;
   const int b = r / a.n_new, j = r - b * a.n_new;
   const int len = lens[b];
-  if (len < 0 || len + a.n_new > a.max_pages * a.S) {
+  if (len < 0 || len > a.max_pages * a.S - a.n_new) {  // (the sum may pass 32 bits)
     if (report && j == 0 && g == 0) raise_status(a.status, BASISKV_DEV_OVERFLOW);
     return x;
   }
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int cap = a.max_pages * a.S;
         for (int b = 0; b < a.B; ++b) {
           const int len = lens[b];
-          if (len < 0 || len + a.n_new > cap)
+          if (len < 0 || len > cap - a.n_new)
             raise_status(a.status, BASISKV_DEV_OVERFLOW);
           else
             a.seq_lens_out[b] = len + a.n_new;

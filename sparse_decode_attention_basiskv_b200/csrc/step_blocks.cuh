@@ -53,7 +53,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int g, int j, 
   }
   const int len = a.seq_lens[b];
   const int cap = a.max_pages * a.S;
-  const bool fits = len >= 0 && len + a.n_new <= cap;
+  const bool fits = len >= 0 && len <= cap - a.n_new;  // (the sum may pass 32 bits)
   const int pos = len + j;
   // block-table entry requested now, used at the end
   const int pp = fits ? a.block_table[(size_t)b * a.max_pages + pos / a.S] : -1;
@@ -152,7 +152,7 @@ __device__ __forceinline__ void append_block_direct(const AppendArgs& a, int g, 
   }
   const int len = a.seq_lens[b];
   const int cap = a.max_pages * a.S;
-  const bool fits = len >= 0 && len + 1 <= cap;
+  const bool fits = len >= 0 && len < cap;
   const int pp = fits ? a.block_table[(size_t)b * a.max_pages + len / a.S] : -1;
   named_bar_sync(bar, kAppendThreads);
   // y[o] = sum_i x[i] F[i][o] for a factor F [rows][outs] (row-major, bf16):

@@ -511,3 +511,20 @@ def test_selected_attention_of_a_bad_length_is_zero():
         assert st == bkv.DEV_BAD_LENGTH
         for b in range(B):
             assert torch.equal(got[b], good[b]) if 0 <= L[b] <= 100 else torch.all(got[b] == 0)
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+def test_lengths_near_the_end_of_32_bits_overflow(length):
+    """The length after a write is not taken in 32 bits."""
+    B, n, Hkv, d, rv, page, mp = 2, 5, 2, 64, 32, 16, 2
+    phys = B * mp
+    dims = dims_of(B, 8, Hkv, d, rv, 16, page, mp, phys)
+    tab = torch.arange(phys, dtype=torch.int32, device="cuda").view(B, mp)
+    rows = [torch.ones(B, n, Hkv, w, dtype=torch.bfloat16, device="cuda") for w in (d, rv)]
+    K, Z = (torch.zeros(bkv.cache4_bytes(dims, w), dtype=torch.uint8, device="cuda")
+            for w in (d, rv))
+    L = torch.tensor([length, 3], dtype=torch.int32, device="cuda")
+    bkv.basiskv_cache4_write(dims, *rows, None, n, L, L, tab, K, Z, None)
+    assert bkv.read_device_status() == bkv.DEV_OVERFLOW
+    assert L.tolist() == [length, 8]
+    assert torch.all(K.view(phys, -1)[:mp] == 0)

@@ -442,3 +442,27 @@ def test_selection_with_tied_scores(levels, T):
             _, ref_sel, _ = oracle_route(pb, b, g, wl.T)
             np.testing.assert_array_equal(sel_r[b, g].cpu().numpy(), ref_sel)
             np.testing.assert_array_equal(sel_d[b, g].cpu().numpy(), ref_sel)
+
+
+@pytest.mark.parametrize("n", [1, 5, 200])
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 3])
+def test_lengths_near_the_end_of_32_bits_overflow(n, length):
+    """The length after an append (one token, a few, a chunk) is not taken in 32
+    bits: such a sequence is skipped whole, the other one appends."""
+    wl = synth.with_sizes(synth.QWEN32B_T64K_B8, B=2, T=160, prefill_tokens=400)
+    pb, layer = gpu_layer(wl, seq_lens=[5, 37])
+    k, v = synth.make_tokens(wl, pb.factors, n, device="cuda", stream_id=5)
+    status_clean()
+    layer.seq_lens[0] = length
+    mine = layer.block_table[0].long()
+    before = layer.K[mine].clone()
+    layer.append(k, v, n)
+    assert bkv.read_device_status() == bkv.DEV_OVERFLOW
+    assert layer.seq_lens.tolist() == [length, 37 + n]
+    assert torch.equal(layer.K[mine].view(torch.uint8), before.view(torch.uint8))
+    if n == 1:  # the fused step, with the same token
+        layer.seq_lens[1] = 37
+        layer.decode(pb.q, k[:, 0].contiguous(), v[:, 0].contiguous(), max_seq_len=160)
+        assert bkv.read_device_status() & bkv.DEV_OVERFLOW
+        assert layer.seq_lens.tolist() == [length, 38]
+        assert torch.equal(layer.K[mine].view(torch.uint8), before.view(torch.uint8))
