@@ -31,8 +31,10 @@ BASISKV_API size_t basiskv_window_workspace_size(const basiskv_dims* dims, int n
  *   cache4   0: K_cache and Z_cache hold bf16, or E4M3 with dims->cache_fp8 = 1;
  *            1: they are 4-bit caches (basiskv_cache4.h; page_size 16 or 32,
  *            dims->cache_fp8 0, no narrow router)
- *   a_out    bf16 [B][n_q][Hq][r_v] (fp32 accumulation, one rounding: with
- *            B * n_q as its batch, the input of basiskv_outproj_sources)
+ *   a_out    bf16 [B][n_q][Hq][r_v] (fp32 scores, sums and accumulation, one
+ *            rounding; the weights enter the products with 16 significant bits
+ *            over bf16 caches and 11 over E4M3 and 4-bit ones, whatever n_q is:
+ *            with B * n_q as its batch, the input of basiskv_outproj_sources)
  * Query tokens with p < 0 (n_q past a sequence's length: a batch padded at the
  * front) see nothing; a row that sees nothing is zero.  A sequence whose length
  * is outside [0, max_seq_len] is taken as empty (BASISKV_DEV_BAD_LENGTH).  A

@@ -300,3 +300,16 @@ def test_bad_pages_are_left_out_of_the_softmax(fmt, n, G, d, rv, page, window, s
             assert_rows(got[b, :, hs].reshape(-1, rv), a, A, X, FMT_WEIGHT[kind],
                         f"{fmt} n{n} b{b} g{g}")
     assert np.all(got[2] == 0)
+
+
+@pytest.mark.parametrize("G,d,rv,page,n", [(4, 128, 64, 16, 40), (8, 64, 128, 32, 200),
+                                           (4, 128, 128, 16, 300), (2, 64, 32, 8, 90)])
+@pytest.mark.parametrize("scale", [1.0, 3.0])
+def test_bf16_prompts_hold_their_weights_in_16_bits(G, d, rv, page, n, scale):
+    """Prompts over bf16 caches are as accurate as single tokens: a weight is its upper
+    8 bits (what they leave is below 2^-7 of it) and a bf16 rounding of the rest, off by
+    at most 2^-16 of the weight."""
+    p = Problem("bf16", 2, G, 2, d, rv, page, [700, 333], n, 0, 0, scale=scale)
+    p.run()
+    assert bkv.read_device_status() == 0
+    p.check(kind="bf16_token")
