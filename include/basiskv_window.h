@@ -41,7 +41,7 @@ BASISKV_API size_t basiskv_window_workspace_size(const basiskv_dims* dims, int n
  * block-table entry out of range leaves its page's tokens out
  * (BASISKV_DEV_BAD_PAGE); entries of pages no query sees are not read, so pages
  * that have left the window may be reused.  Cached rows that some query of the
- * call sees must be finite.  dims->route_page, sink_pages and recent_pages are
+ * call sees must be finite, their latents at most 2^64 in magnitude.  dims->route_page, sink_pages and recent_pages are
  * ignored; any page_size of basiskv.h. */
 BASISKV_API int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n_q,
                                       const int32_t* seq_lens, int max_seq_len,

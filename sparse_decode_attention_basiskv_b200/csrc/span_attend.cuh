@@ -35,7 +35,7 @@
 // become PV's B operand with one 8x8 transposition per 8 tokens.
 //
 // The running reference moves only when a score passes it by a wide margin
-// (2^15 or 2^64 in the weights, which the operands' types hold): then the warp
+// (2^15 or 2^32 in the weights, which the operands' types hold): then the warp
 // takes the rows' maxima over their lanes and rescales; all other units cost
 // one vote.
 //
@@ -69,11 +69,12 @@ namespace {
 constexpr int kSpThreads = kLineMaxSeqs;  // a thread scans a sequence's length
 constexpr int kSpWarps = kSpThreads / 32;
 // How far (log2) scores may pass the reference before it moves: the weights then
-// reach 2^15 in f16, 2^64 in bf16, whose products and sums stay far inside
-// fp32's range, at the same relative precision.
+// reach 2^15 in f16, 2^32 in bf16, at the same relative precision, and their products
+// and sums stay inside fp32's range: over bf16 caches for latents up to 2^64 and 2^30
+// tokens.  (2^64, at the same times, overflowed from latents of 2^60 on.)
 template <int FMT>
 constexpr float sp_slack() {
-  return FMT == kSpanBf16 ? 64.f : 15.f;
+  return FMT == kSpanBf16 ? 32.f : 15.f;
 }
 
 // Tokens of a unit: 32 over 4-bit caches, and over E4M3 ones where 17 to 32 rows

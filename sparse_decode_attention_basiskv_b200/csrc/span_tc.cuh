@@ -79,11 +79,12 @@ namespace {
 constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;  // two row tiles
 // How far (log2) scores may pass the reference before it moves: the weights then
-// reach 2^15 in f16, 2^64 in bf16, whose products and sums stay far inside
-// fp32's range, at the same relative precision.
+// reach 2^15 in f16, 2^32 in bf16, at the same relative precision, and their products
+// and sums stay inside fp32's range: over bf16 caches for latents up to 2^64 and 2^30
+// tokens.  (2^64, at the same times, overflowed from latents of 2^60 on.)
 template <int FMT>
 constexpr float tc_slack() {
-  return FMT == kSpanBf16 ? 64.f : 15.f;
+  return FMT == kSpanBf16 ? 32.f : 15.f;
 }
 
 template <int D, int RV>

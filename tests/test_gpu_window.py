@@ -313,3 +313,23 @@ def test_bf16_prompts_hold_their_weights_in_16_bits(G, d, rv, page, n, scale):
     p.run()
     assert bkv.read_device_status() == 0
     p.check(kind="bf16_token")
+
+
+@pytest.mark.parametrize("n", [1, 6, 100])
+def test_large_latents(n):
+    """Latents of 2^70, where a token in 200 scores 60 (log2) above the others: the
+    sums stay finite, whichever token a reference was taken from."""
+    lens = [700, 650, 600, 690]
+    p = Problem("bf16", 4, 4, 8, 64, 32, 16, lens, n, 0, 0)
+    table = p.table.cpu().numpy()
+    rng = np.random.default_rng(5)
+    spike = 60 / 1.4427 * 8 / 64  # of all 64 columns, under queries of ones
+    p.K = Paged([spike * (rng.random((L, 8, 1)) < 1 / 200) * np.ones((1, 1, 64)) for L in lens],
+                "bf16", 16, table, p.dims.num_phys_pages)
+    p.Z = Paged([rng.standard_normal((L, 8, 32)) * 2.0 ** 70 for L in lens], "bf16", 16, table,
+                p.dims.num_phys_pages)
+    p.q = bf16(np.ones((4, n, 32, 64)))
+    p.qd = p.q.cuda()
+    p.run()
+    assert bkv.read_device_status() == 0
+    p.check()
