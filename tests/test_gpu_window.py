@@ -333,3 +333,15 @@ def test_large_latents(n):
     p.run()
     assert bkv.read_device_status() == 0
     p.check()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("G,d,rv,page", [(4, 128, 128, 16), (8, 128, 128, 32), (4, 128, 32, 32),
+                                         (8, 128, 32, 16), (2, 128, 96, 16), (1, 64, 96, 32)])
+@pytest.mark.parametrize("n,window,sink,lens", [(80, 0, 0, [700, 33, 260]),
+                                                (300, 130, 70, [650, 301])])
+def test_prompts_of_every_width(fmt, G, d, rv, page, n, window, sink, lens):
+    """The prompt kernel's instances differ in their stages and in where the queries
+    lie (r_v 128 at d 128 has none of them in tensor memory)."""
+    p = _go(fmt, len(lens), G, 2, d, rv, page, lens, n, window, sink)
+    p.check(kind="bf16_token" if fmt == "bf16" else fmt)
