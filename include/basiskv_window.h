@@ -16,7 +16,10 @@ extern "C" {
  * sequence, contexts of at most max_seq_len tokens and this mask; 0 when the
  * arguments are invalid.  It holds for a call with these arguments, whatever the
  * lengths: the work is split otherwise for other ones, and a smaller
- * max_seq_len may need more. */
+ * max_seq_len may need more.  Whatever max_seq_len and the mask, it is at most
+ *   (512 + B * Hkv) * R * (r_v + 4) * 4 bytes  for R = n_q * Hq / Hkv <= 16,
+ *   4 * SMs * 256 * (r_v + 2) * 4 bytes        for R > 32 (79 MB at r_v 128, 148 SMs),
+ * and the larger of the two between, rounded up to 256 bytes. */
 BASISKV_API size_t basiskv_window_workspace_size(const basiskv_dims* dims, int n_q,
                                                  int max_seq_len, int sink_tokens, int window);
 
@@ -41,8 +44,9 @@ BASISKV_API size_t basiskv_window_workspace_size(const basiskv_dims* dims, int n
  * block-table entry out of range leaves its page's tokens out
  * (BASISKV_DEV_BAD_PAGE); entries of pages no query sees are not read, so pages
  * that have left the window may be reused.  Cached rows that some query of the
- * call sees must be finite, their latents at most 2^64 in magnitude.  dims->route_page, sink_pages and recent_pages are
- * ignored; any page_size of basiskv.h. */
+ * call sees must be finite, their latents at most 2^64 in magnitude.
+ * dims->route_page, sink_pages and recent_pages are ignored; any page_size of
+ * basiskv.h. */
 BASISKV_API int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n_q,
                                       const int32_t* seq_lens, int max_seq_len,
                                       const int32_t* block_table, const void* K_cache,

@@ -12,10 +12,17 @@
 using namespace basiskv;
 
 // Rounds of the SMs take whole items while they are full.  What is left over is
-// cut so that the rounds it takes are short and few: a run costs its KV tiles
-// and about 5 tiles' time for its start and end (measured: 16,000 and 3,500
-// clocks at d 128, r_v 64), and keeps 4 tiles at least.
-TcPlan basiskv::tc_plan(int B, int Hkv, int G, int n_tot, int max_seq_len, int sink, int window) {
+// cut where that pays: a run costs its KV tiles and about 5 tiles' time for its start
+// and end (measured: 16,000 and 3,500 clocks at d 128, r_v 64), the join about 2
+// tiles' time and, for writing and reading a run's partials, (r_v + 2) / 6200; a run
+// keeps 4 tiles at least, and there are 4 runs an SM at most, which bounds the
+// workspace.  Whole / as cut here, us, bf16 r_v 64, r_v 128, 4 bits r_v 64, r_v 128:
+// 56 items over 16K tokens (5 runs each) 309 / 149, 408 / 196, 289 / 138, 328 / 163;
+// 24 over 4K (6) 80 / 32, 104 / 38, 72 / 30, 76 / 33; 8 over 32K (16) 578 / 59, 923 / 75,
+// 516 / 53, 547 / 58.  128 items stay whole: in 8 runs each, 37,000 tokens take 690
+// for 696, 960 for 903, 602 for 597, 714 for 684.
+TcPlan basiskv::tc_plan(int B, int Hkv, int G, int n_tot, int max_seq_len, int sink, int window,
+                        int r_v) {
   const int sms = num_sms(), tq2 = 256 / G;
   const long long items = (long long)B * Hkv * ((n_tot + tq2 - 1) / tq2);
   TcPlan p{(int)(items / sms * sms), (int)(items % sms), 1};
@@ -23,10 +30,12 @@ TcPlan basiskv::tc_plan(int B, int Hkv, int G, int n_tot, int max_seq_len, int s
   long long span = max_seq_len;
   if (window > 0 && (long long)window + tq2 + sink < span) span = (long long)window + tq2 + sink;
   const long long tiles = (span + 127) / 128 + 1;
-  long long best = -1;
-  for (int ns = 1; ns <= 64 && (ns == 1 || tiles / ns >= 4); ++ns) {
-    const long long rounds = ((long long)p.tail * ns + sms - 1) / sms;
-    const long long cost = rounds * ((tiles + ns - 1) / ns + 5);
+  long long best = -1;  // in hundredths of a tile's time
+  for (int ns = 1; ns <= 64 && (ns == 1 || (tiles / ns >= 4 && p.tail * ns <= kTcMaxRuns * sms));
+       ++ns) {
+    const long long runs = (long long)p.tail * ns, rounds = (runs + sms - 1) / sms;
+    long long cost = 100 * rounds * ((tiles + ns - 1) / ns + 5);
+    if (ns > 1) cost += 200 + runs * (r_v + 2) / 62;
     if (best < 0 || cost < best) {
       best = cost;
       p.ns = ns;
@@ -147,7 +156,7 @@ size_t window_bytes(const basiskv_dims* d, int n_q, int max_seq_len, int sink, i
   const int G = d->Hq / d->Hkv;
   const Mask m = window_mask(max_seq_len, sink, window);
   if (window_streams(d, n_q, max_seq_len, m)) return span_partial_bytes(d, n_q * G);
-  const TcPlan plan = tc_plan(d->B, d->Hkv, G, n_q, max_seq_len, m.sink, m.window);
+  const TcPlan plan = tc_plan(d->B, d->Hkv, G, n_q, max_seq_len, m.sink, m.window, d->r_v);
   const size_t n = tc_partial_bytes(plan, d->r_v);
   return n > 256 ? (n + 255) & ~size_t(255) : 256;
 }

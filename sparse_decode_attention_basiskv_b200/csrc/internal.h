@@ -303,7 +303,8 @@ cudaError_t launch_span_q4_p32(const SpanArgs& a, cudaStream_t st, bool pdl);
 struct TcPlan {
   int full, tail, ns;
 };
-TcPlan tc_plan(int B, int Hkv, int G, int n_tot, int max_seq_len, int sink, int window);
+constexpr int kTcMaxRuns = 4;  // of the cut items, an SM
+TcPlan tc_plan(int B, int Hkv, int G, int n_tot, int max_seq_len, int sink, int window, int r_v);
 inline size_t tc_partial_bytes(const TcPlan& p, int r_v) {
   return p.ns > 1 ? (size_t)p.tail * p.ns * 256 * (r_v + 2) * 4 : 0;
 }

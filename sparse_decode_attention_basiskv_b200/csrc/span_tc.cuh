@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(256) span_tc_merge_kernel(SpanArgs a, TcPlan p
 
 template <int FMT, int D, int RV>
 cudaError_t launch_span_tc_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
-  const TcPlan plan = tc_plan(a.B, a.Hkv, a.G, a.n_tot, a.max_seq_len, a.sink, a.window);
+  const TcPlan plan = tc_plan(a.B, a.Hkv, a.G, a.n_tot, a.max_seq_len, a.sink, a.window, a.r_v);
   cudaError_t e = cudaFuncSetAttribute(span_tc_kernel<FMT, D, RV>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)TcGeom<D, RV>::kSmem);

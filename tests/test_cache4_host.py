@@ -239,3 +239,22 @@ def test_binding_refuses_tensors_elsewhere(monkeypatch):
 
     with pytest.raises(ValueError, match="cuda:1"):
         bkv._here(None, None, Elsewhere())
+
+
+def test_window_workspace_is_bounded(lib):
+    """Prompts: at most four runs an SM (148 of them here, where no GPU is found), and
+    none where the split would gain less than its join costs."""
+    sms, worst = 148, 0
+    for r_v, B, Hq, n in itertools.product((64, 128), (1, 2, 3, 4, 5, 7, 9, 16), (8, 32, 64),
+                                           (40, 130, 200, 257, 1000)):
+        for bound in (400, 4096, 34000, 37000, 131072, 1 << 20):
+            d = _dims(B=B, Hq=Hq, Hkv=8, r_v=r_v, page_size=32, max_pages_per_seq=1 << 15,
+                      num_phys_pages=1 << 16)
+            for window in (0, 4096):
+                size = bkv.window_workspace_size(d, n, bound, 4, window)
+                assert 256 <= size <= 4 * sms * 256 * (r_v + 2) * 4 + 256
+                worst = max(worst, size)
+    assert worst > 2 * sms * 256 * 66 * 4  # splits are taken
+    for r_v in (64, 128):
+        d = _dims(B=4, Hq=32, Hkv=8, r_v=r_v, max_pages_per_seq=4096, num_phys_pages=1 << 15)
+        assert {bkv.window_workspace_size(d, 200, x, 0, 0) for x in (34000, 37000, 60000)} == {256}
