@@ -17,6 +17,8 @@
 namespace basiskv {
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
+// What a block that has given up waits for its own copies and products in flight.
+constexpr unsigned long long kDrainNs = 10000000ull;  // 10 ms
 
 __device__ __forceinline__ unsigned long long global_ns() {
   unsigned long long t;

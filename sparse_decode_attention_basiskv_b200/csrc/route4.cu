@@ -294,8 +294,10 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
       ++slot;
       if (slot == NB || slot == NST) {  // half the ring has been read by every lane
         __syncwarp();
-        issue(k_next, slot - NB);
-        k_next += NB;
+        if (landing) {
+          issue(k_next, slot - NB);
+          k_next += NB;
+        }
         if (slot == NST) {
           slot = 0;
           phase ^= 1;
@@ -303,6 +305,10 @@ __global__ void __launch_bounds__(kR4Threads, r4_ctas<RV + RK, NJ>())
       }
     }
   }
+  // a wait has run out: no copy may still be on its way into this block's memory
+  if (!landing)
+    for (int k = k_next - NST; k < min(k_next, run); ++k)
+      mbar_wait(bars + warp * NST + k % NST, (k / NST) & 1, a.status, kDrainNs);
 }
 
 template <int RV, int RK, int NJ, bool ONE>

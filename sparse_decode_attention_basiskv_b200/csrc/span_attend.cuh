@@ -380,7 +380,9 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
   };
 
   int k_next = 0, slot_next = 0;  // the next unit to request, and its slot
+  bool landing = true;  // no wait has run out yet (the others would, too)
   auto request = [&]() {
+    if (!landing) return;
     issue(k_next++, slot_next);
     slot_next = slot_next + 1 == NST ? 0 : slot_next + 1;
   };
@@ -388,7 +390,6 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) request();
   int slot = 0;
-  bool landing = true;  // no wait has run out yet (the others would, too)
   uint32_t phase = 0;  // of the slots' barriers in this turn of the ring
 
   // 4-bit units: byte offsets of half 1's codes and of the halves' scales
@@ -881,6 +882,10 @@ __global__ void __launch_bounds__(kSpThreads, sp_ctas<FMT, NR>()) span_kernel(Sp
     }
     seg = item_end;
   }
+  // a wait has run out: no copy may still be on its way into this block's memory
+  if (BULK && !landing)
+    for (int k = max(0, k_next - NST); k < min(k_next, n_units); ++k)
+      mbar_wait(bars + warp * NST + k % NST, (k / NST) & 1, a.status, kDrainNs);
 }
 
 // Joins the partials of the items that several CTAs share; rows of items

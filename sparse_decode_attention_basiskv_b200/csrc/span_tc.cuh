@@ -380,6 +380,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
             if (u & 1) next(kst, kph);
           }
         }
+        if (!ok) {  // a wait has run out: tensor memory goes once the products are done
+          if (lead) tc_commit_to(&scored[t]);
+          mbar_wait(&scored[t], scored_ph, a.status, kDrainNs);
+        }
       };
       if (gap)
         issue(std::true_type{});
