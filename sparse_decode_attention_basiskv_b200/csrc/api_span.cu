@@ -132,33 +132,48 @@ Mask window_mask(int max_seq_len, int sink, int window) {
   return {sink < max_seq_len ? sink : max_seq_len, window < max_seq_len ? window : 0};
 }
 
-// Which calls are streamed, by the rows (query tokens times group heads) that
-// share a Key; the others go to the tensor cores, whose tiles hold 128 rows.
-// Always up to 16 rows; 17 to 32 where the call may read kStreamTokens tokens
-// or more.  Both sides, us, 7 x 8 heads and 8196 tokens, r_v 64 / 128: 20 rows
-// 51 / 59 against 78 / 143 (E4M3), 59 / 72 against 74 / 100 (bf16), 47 / 57
-// against 84 / 100 (4 bits); 32 rows 57 / 92 against 79 / 145, 72 / 104 against
-// 74 / 100, 57 / 88 against 84 / 102.  8 heads and 1028 tokens, where the code
-// itself is fetched once: 16 rows 22 / 25 against 22 / 31 (E4M3), 20 rows
-// 27 / 29 against 22 / 31, 32 rows 29 / 37 against 23 / 31.
-constexpr long long kStreamTokens = 65536;
-bool window_streams(const basiskv_dims* d, int n_q, int max_seq_len, Mask m) {
+// Which calls are streamed, by the rows (query tokens times group heads) that share a
+// Key and by the tokens of all heads that the call may read; the others go to the
+// tensor cores, whose tiles hold 128 rows.
+//
+// Always up to 16 rows.  17 to 24 rows from 128K tokens on, 25 to 32 from 256K (r_v
+// 128: 384K; over bf16 caches with r_v above 64 never): there a lane's queries and
+// accumulators fill its registers.  Both sides, streamed / tensor cores, us, captured
+// calls, d 128, r_v 64 unless said:
+//   16 rows, 64K tokens (1 x 8 heads)  bf16 18.6 / 22.3   E4M3 17.8 / 23.3   4 bits 17.4 / 21.7
+//   24 rows, 64K                       bf16 25.4 / 22.9   E4M3 24.0 / 24.3   4 bits 25.2 / 22.3
+//            128K                      bf16 30.4 / 30.9   E4M3 27.2 / 31.3   4 bits 28.1 / 28.9
+//            448K (7 x 8 heads)        bf16 51.1 / 68.0   E4M3 38.5 / 79.2   4 bits 37.5 / 71.6
+//   32 rows, 128K                      bf16 35.0 / 30.0   E4M3 31.8 / 31.3   4 bits 33.0 / 28.9
+//            256K                      bf16 47.2 / 44.6   E4M3 39.6 / 48.5   4 bits 40.1 / 41.5
+//            448K                      bf16 61.3 / 68.3   E4M3 46.1 / 79.5   4 bits 45.5 / 71.2
+//   32 rows, r_v 128, 256K             bf16 69.5 / 52.6   E4M3 63.4 / 72.5   4 bits 59.2 / 48.0
+//            448K                      bf16 93.8 / 86.8   E4M3 78.1 / 128    4 bits 75.1 / 85.2
+//            1M                        bf16 184 / 158     E4M3 147 / 243     4 bits 142 / 159
+//   32 rows, r_v 96, 1M                bf16 173 / 146     E4M3 98 / 171      4 bits 96 / 151
+bool window_streams(const basiskv_dims* d, int n_q, int max_seq_len, Mask m, bool cache4) {
   const int G = d->Hq / d->Hkv;
   if (n_q <= 16 / G) return true;
   if (n_q > kSpanMaxRows / G) return false;
   if (d->cache_fp8 && d->page_size < 16) return false;  // two pages of 16 make a unit there
   const long long seen = (long long)m.window + n_q + m.sink;
   const long long span = m.window > 0 && seen < max_seq_len ? seen : max_seq_len;
-  return span * d->B * d->Hkv >= kStreamTokens;
+  const long long tokens = span * d->B * d->Hkv;
+  if (n_q <= 24 / G) return tokens >= 128 << 10;
+  if (!d->cache_fp8 && !cache4 && d->r_v > 64) return false;
+  return tokens >= (d->r_v == 128 ? 384 : 256) << 10;
 }
 
 size_t window_bytes(const basiskv_dims* d, int n_q, int max_seq_len, int sink, int window) {
   const int G = d->Hq / d->Hkv;
   const Mask m = window_mask(max_seq_len, sink, window);
-  if (window_streams(d, n_q, max_seq_len, m)) return span_partial_bytes(d, n_q * G);
+  // (which caches the call will have, bf16 or 4 bits, is not known here)
+  const bool any = window_streams(d, n_q, max_seq_len, m, true);
+  const size_t streamed = any ? span_partial_bytes(d, n_q * G) : 256;
+  if (any && window_streams(d, n_q, max_seq_len, m, false)) return streamed;
   const TcPlan plan = tc_plan(d->B, d->Hkv, G, n_q, max_seq_len, m.sink, m.window, d->r_v);
   const size_t n = tc_partial_bytes(plan, d->r_v);
-  return n > 256 ? (n + 255) & ~size_t(255) : 256;
+  return n > streamed ? (n + 255) & ~size_t(255) : streamed;
 }
 
 }  // namespace
@@ -375,7 +390,7 @@ int basiskv_attend_window(const basiskv_dims* dims, const basiskv_bf16* q, int n
   a.n_tot = n_q;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool pdl = pdl_allowed();
-  if (window_streams(dims, n_q, max_seq_len, m))
+  if (window_streams(dims, n_q, max_seq_len, m, cache4))
     return status_of(cache4 ? launch_span_q4(a, st, pdl)
                             : dims->cache_fp8 ? launch_span_e4m3(a, st, pdl)
                                               : launch_span_bf16(a, st, pdl));

@@ -954,28 +954,34 @@ cudaError_t launch_span_t(const SpanArgs& a, cudaStream_t st, bool pdl) {
                   dim3(kSpThreads), 0, st, pdl, a, (int)grid);
 }
 
+template <int FMT, int D, int RV, bool ONE>
+cudaError_t launch_span_rows(const SpanArgs& a, cudaStream_t st, bool pdl) {
+  switch ((a.n_tot * a.G + 7) / 8) {  // tiles of 8 rows
+    case 1: return launch_span_t<FMT, D, RV, 1, ONE>(a, st, pdl);
+    case 2: return launch_span_t<FMT, D, RV, 2, ONE>(a, st, pdl);
+    case 3: return launch_span_t<FMT, D, RV, 3, ONE>(a, st, pdl);
+    default:
+      if constexpr (FMT == kSpanBf16 && RV > 64)
+        return cudaErrorInvalidValue;  // not streamed
+      else
+        return launch_span_t<FMT, D, RV, 4, ONE>(a, st, pdl);
+  }
+}
+
+template <int FMT, int D, bool ONE>
+cudaError_t launch_span_width(const SpanArgs& a, cudaStream_t st, bool pdl) {
+  switch (a.r_v) {
+    case 32: return launch_span_rows<FMT, D, 32, ONE>(a, st, pdl);
+    case 64: return launch_span_rows<FMT, D, 64, ONE>(a, st, pdl);
+    case 96: return launch_span_rows<FMT, D, 96, ONE>(a, st, pdl);
+    default: return launch_span_rows<FMT, D, 128, ONE>(a, st, pdl);
+  }
+}
+
 template <int FMT, bool ONE = false>
 cudaError_t launch_span_fmt(const SpanArgs& a, cudaStream_t st, bool pdl) {
-  const int tiles = (a.n_tot * a.G + 7) / 8;  // of 8 rows
-#define BKV_SPAN_NR(DD, RR)                                                  \
-  return tiles == 1   ? launch_span_t<FMT, DD, RR, 1, ONE>(a, st, pdl)       \
-         : tiles == 2 ? launch_span_t<FMT, DD, RR, 2, ONE>(a, st, pdl)       \
-         : tiles == 3 ? launch_span_t<FMT, DD, RR, 3, ONE>(a, st, pdl)       \
-                      : launch_span_t<FMT, DD, RR, 4, ONE>(a, st, pdl)
-#define BKV_SPAN_RV(DD)                                                      \
-  switch (a.r_v) {                                                           \
-    case 32: BKV_SPAN_NR(DD, 32);                                            \
-    case 64: BKV_SPAN_NR(DD, 64);                                            \
-    case 96: BKV_SPAN_NR(DD, 96);                                            \
-    default: BKV_SPAN_NR(DD, 128);                                           \
-  }
-  if (a.d == 64) {
-    BKV_SPAN_RV(64)
-  } else {
-    BKV_SPAN_RV(128)
-  }
-#undef BKV_SPAN_RV
-#undef BKV_SPAN_NR
+  return a.d == 64 ? launch_span_width<FMT, 64, ONE>(a, st, pdl)
+                   : launch_span_width<FMT, 128, ONE>(a, st, pdl);
 }
 
 }  // namespace

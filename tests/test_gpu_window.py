@@ -345,3 +345,23 @@ def test_prompts_of_every_width(fmt, G, d, rv, page, n, window, sink, lens):
     lie (r_v 128 at d 128 has none of them in tensor memory)."""
     p = _go(fmt, len(lens), G, 2, d, rv, page, lens, n, window, sink)
     p.check(kind="bf16_token" if fmt == "bf16" else fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bound", [2500, 4300, 6500])
+@pytest.mark.parametrize("G,d,rv,page,n", [(4, 128, 64, 16, 5), (8, 64, 96, 32, 3),
+                                           (8, 128, 128, 32, 4), (1, 64, 128, 16, 31),
+                                           (4, 64, 32, 32, 7), (2, 128, 96, 16, 13)])
+def test_drafts_whose_bound_passes_the_contexts(fmt, bound, G, d, rv, page, n):
+    """17 to 32 rows a group with bounds on the lengths on both sides of the sizes from
+    which they are streamed (64 times 2048, 4096 and 6144 tokens): the same answers."""
+    lens = [700, 3, 0, 17, 512, 429, 300, 699]
+    p = Problem(fmt, 8, G, 8, d, rv, page, lens, n, 0, 0)
+    wide = torch.full((8, -(-bound // page)), -1, dtype=torch.int32, device="cuda")
+    wide[:, :p.table.shape[1]] = p.table
+    p.table, p.dims.max_pages_per_seq, p.msl = wide, wide.shape[1], bound
+    p.ws = torch.full((bkv.window_workspace_size(p.dims, n, bound, 0, 0),), 0x7F,
+                      dtype=torch.uint8, device="cuda")
+    p.run()
+    assert bkv.read_device_status() == 0
+    p.check(kind="bf16_token" if fmt == "bf16" else fmt)
