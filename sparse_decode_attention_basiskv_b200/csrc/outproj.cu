@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "tcgen05.cuh"
 
 namespace basiskv {
 
@@ -34,47 +35,6 @@ constexpr int op_stages() {
              : 8;
 }
 constexpr int kOpATile = kOpBM * kOpBK * 2;  // 16 KB
-
-// tcgen05 instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B,
-// both K-major, N>>3 at bit 17, M>>4 at bit 24.
-__host__ __device__ constexpr uint32_t make_idesc(int M, int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-
-// Shared-memory matrix descriptor for a K-major tile with 128-byte swizzle:
-// rows of 128 bytes, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3fff);  // start address
-  d |= (uint64_t)1 << 16;                   // leading byte offset (unused here)
-  d |= (uint64_t)(1024 >> 4) << 32;         // stride byte offset
-  d |= (uint64_t)1 << 46;                   // descriptor version (sm_100)
-  d |= (uint64_t)2 << 61;                   // SWIZZLE_128B
-  return d;
-}
-
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_mma(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(tmem_d),
-      "l"(da), "l"(db), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
@@ -131,9 +91,9 @@ __global__ void __launch_bounds__(kOpThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  tc_fence_before();
+  tc_fence_before_sync();
   __syncthreads();
-  tc_fence_after();
+  tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   // Only the producer (before the latent tiles) and the length update wait
   // for the earlier kernels: W' is a weight no kernel of the step writes, so
@@ -170,7 +130,7 @@ __global__ void __launch_bounds__(kOpThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ------------------------------------------ MMA issue
-      const uint32_t idesc = make_idesc(kOpBM, BN);
+      const uint32_t idesc = tc_idesc(kOpBM, BN, true, false);
       bool ok = true;
       for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
         const int s = it % kOpStages;
@@ -178,21 +138,21 @@ __global__ void __launch_bounds__(kOpThreads, 1)
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint64_t da = make_sdesc(smem_u32(a_tiles + s * kOpATile));
-        const uint64_t db = make_sdesc(smem_u32(b_tiles + s * kBTile));
+        tc_fence_after_sync();
+        const uint64_t da = tc_sdesc(smem_u32(a_tiles + s * kOpATile));
+        const uint64_t db = tc_sdesc(smem_u32(b_tiles + s * kBTile));
 #pragma unroll
         for (int k = 0; k < kOpBK / 16; ++k)  // 32 bytes of K per instruction
-          tc_mma(tmem, da + 2 * k, db + 2 * k, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
-        tc_commit(&empty[s]);
+          tc_mma_ss(tmem, da + 2 * k, db + 2 * k, idesc, kb > kb0 || k > 0);
+        tc_commit_to(&empty[s]);
       }
-      if (ok) tc_commit(accum);
+      if (ok) tc_commit_to(accum);
     }
   } else {  // ------------------------------------------------------ epilogue
     const int quarter = warp & 3;  // TMEM lanes this warp may read
     const int row = quarter * 32 + lane;
     if (mbar_wait(accum, 0, a.status)) {
-      tc_fence_after();
+      tc_fence_after_sync();
 #pragma unroll
       for (int c0 = 0; c0 < BN; c0 += 16) {
         float v[16];
@@ -256,10 +216,10 @@ __global__ void __launch_bounds__(kOpThreads, 1)
       if (tid == 0) a.cnt[blockIdx.x] = 0;  // ready for the next call
     }
   }
-  tc_fence_before();
+  tc_fence_before_sync();
   __syncthreads();
   if (warp == 1) {
-    tc_fence_after();
+    tc_fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
                  : "memory");

@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "tcgen05.cuh"
 
 namespace basiskv {
 
@@ -132,28 +133,12 @@ constexpr int kTcThreads = 32 * (kTcKeyWarp0 + kTcKeyWarps);
 constexpr int kTcBM = 128, kTcBK = 64;
 constexpr int kTcABytes = kTcBM * kTcBK * 2;  // one ring slot: 128 rows x 128 bytes
 constexpr int kTcMaxSlots = 12;
-constexpr unsigned long long kTcDrainNs = 10000000ull;  // waits for copies in flight at exit
 
 // Arrival counts for the in-kernel length update, one slot per call in
 // flight (the host hands slots out round-robin): zero when the library
 // loads, and reset by the CTA that completes a call's count.
 constexpr int kTcArriveSlots = 64;
 __device__ unsigned int g_tc_arrive[kTcArriveSlots];
-
-__host__ __device__ constexpr uint32_t tc_idesc(int M, int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ uint64_t tc_sdesc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3fff);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
 
 // Shared memory: W_app's v k-blocks (d/64 tiles of N x 128 bytes), its k
 // k-blocks (d/64 tiles of r_k x 128 bytes), the ring, the epilogue's
@@ -236,13 +221,6 @@ __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-
 __global__ void __launch_bounds__(kTcThreads, 1)
     append_tc_kernel(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmW,
@@ -296,9 +274,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  tc_fence_before_sync();
   __syncthreads();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   // The next launch may be scheduled now: it waits for this grid to
@@ -375,10 +353,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     // drain: every copy issued must have landed before the CTA exits
     for (int u = it - 1; u >= 0 && u >= it - slots; --u)
-      mbar_wait(&full[u % slots], (u / slots) & 1, a.status, kTcDrainNs);
-    if (wl > 0) mbar_wait(wfull, (wl - 1) & 1, a.status, kTcDrainNs);
+      mbar_wait(&full[u % slots], (u / slots) & 1, a.status, kDrainNs);
+    if (wl > 0) mbar_wait(wfull, (wl - 1) & 1, a.status, kDrainNs);
   } else if (warp == 1 && lane == 0) {  // ------------------------------ MMA
-    const uint32_t idesc = tc_idesc(kTcBM, N), idesc_e = tc_idesc(kTcBM, a.r_k);
+    const uint32_t idesc = tc_idesc(kTcBM, N, true, false),
+                   idesc_e = tc_idesc(kTcBM, a.r_k, true, false);
     int it = 0, wl = 0, cur_g = -1, lt = 0;
     bool ok = true;
     for (int item = i0; item < i1 && ok; ++item, ++lt) {
@@ -392,12 +371,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lt >= 2 && !(ok = mbar_wait_or_abort(&tempty[buf], ((lt >> 1) - 1) & 1, a.status,
                                                abort_flag)))
         break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      tc_fence_after_sync();
       const uint32_t dt = tmem + (uint32_t)(buf * acc_cols);
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const int s = it % slots;
         if (!(ok = mbar_wait_or_abort(&full[s], (it / slots) & 1, a.status, abort_flag))) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        tc_fence_after_sync();
         // a v k-block feeds all N columns; a k k-block only the e columns
         const bool from_v = kb < nkb / 2;
         const uint64_t da = tc_sdesc(smem_u32(ring + s * kTcABytes));
@@ -406,26 +385,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t dk = from_v ? dt : dt + (uint32_t)a.r_v;
         const uint32_t ik = from_v ? idesc : idesc_e;
 #pragma unroll
-        for (int k = 0; k < kTcBK / 16; ++k) {
-          const uint32_t acc = (kb > 0 || k > 0) ? 1u : 0u;
-          asm volatile(
-              "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
-              " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(dk),
-              "l"(da + 2 * k), "l"(db + 2 * k), "r"(ik), "r"(acc)
-              : "memory");
-        }
+        for (int k = 0; k < kTcBK / 16; ++k)
+          tc_mma_ss(dk, da + 2 * k, db + 2 * k, ik, kb > 0 || k > 0);
         // slot s is released when these MMAs complete (and, for a k slot,
         // once the Key warps have copied it out)
-        tc_commit(&empty[s]);
+        tc_commit_to(&empty[s]);
         if (from_v) mbar_arrive_n(&empty[s], kTcKeyWarps);
       }
       if (!ok) break;
-      tc_commit(&tfull[buf]);
-      if (item + 1 < i1 && (item + 1) / n_mt != g) tc_commit(wempty);
+      tc_commit_to(&tfull[buf]);
+      if (item + 1 < i1 && (item + 1) / n_mt != g) tc_commit_to(wempty);
     }
     // drain: one more commit tracks every MMA this thread issued
-    tc_commit(drain);
-    mbar_wait(drain, 0, a.status, kTcDrainNs);
+    tc_commit_to(drain);
+    mbar_wait(drain, 0, a.status, kDrainNs);
   } else if (warp >= 2 && warp < kTcKeyWarp0) {  // ----------------------- epilogue
     const int quarter = warp & 3;  // this warp's 32 TMEM lanes = tile rows
     const int zs = a.zsplit, es = a.esplit;
@@ -475,7 +448,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = mbar_wait_or_abort(&tfull[buf], (lt >> 1) & 1, a.status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      tc_fence_after_sync();
       // accumulator -> cache element type -> this lane's rows of the parts
       const uint32_t ta = tmem + (uint32_t)(buf * acc_cols) + ((uint32_t)(quarter * 32) << 16);
       for (int c0 = 0; c0 < N; c0 += 16) {
@@ -518,7 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       // the accumulator buffer is free for the MMA two tiles on
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      tc_fence_before_sync();
       // the staged rows are visible to the copy engine once every lane is here
       fence_proxy_async();
       __syncwarp();
@@ -622,10 +595,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     bulk_wait_all();
   }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  tc_fence_before_sync();
   __syncthreads();
   if (warp == 1) {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tc_fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(tmem_cols)
                  : "memory");

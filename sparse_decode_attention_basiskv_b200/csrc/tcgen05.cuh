@@ -1,5 +1,5 @@
-// tcgen05 helpers of the windowed prompt attention: descriptors, MMA issue,
-// tensor-memory loads and stores.
+// tcgen05 helpers of the prompt attention, the prompt append and the
+// out-projection: descriptors, MMA issue, tensor-memory loads and stores.
 #pragma once
 
 #include "common.cuh"
