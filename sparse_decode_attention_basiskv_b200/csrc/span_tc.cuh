@@ -27,15 +27,15 @@
 // ahead of what they hand over.
 //
 // Precision: scores, maxima and sums in fp32.  Over E4M3 and 4-bit caches the weights
-// are rounded to f16 for P Z (2^-12 of a weight).  Over bf16 ones a weight is its upper
-// 8 bits and a bf16 rounding of the rest (16 bits, a second product), so that a
-// prompt is as accurate as a token.  With weights of 8 bits the chunk below takes 273
-// us instead of 321, and its error against 64 bits is 2.2e-3 instead of 1.7e-3, of
-// which 1.7e-3 is the output's rounding; with a row's sum taken over such rounded
-// weights (which makes rows of one large weight exact) it takes 296.
+// are rounded to f16 for P Z (2^-12 of a weight).  Over bf16 ones a weight is its bf16
+// rounding and a rounding of the rest (16 bits, a second product), so that a prompt is
+// as accurate as a token.  With weights of 8 bits the chunk below takes 273 us instead
+// of 305, and its error against 64 bits is 2.2e-3 instead of 1.7e-3, of which 1.7e-3 is
+// the output's rounding; with a row's sum taken over such weights (which makes rows
+// of one large weight exact) it takes 296.
 //
-// Tensor memory: per row tile two slots of 64 columns for S, P over its S (the
-// remainders in the upper 32 columns), r_v for O, and Q in what is left (all of it for r_v up to 64, d
+// Tensor memory: per row tile two slots of 64 columns for S, P over its S (bf16: 32
+// tokens' weights, their remainders, the other 32 tokens'), r_v for O, and Q in what is left (all of it for r_v up to 64, d
 // 128; the other k-steps read Q from shared memory).  Q K^T of step i + 2
 // follows P Z of step i on the tensor cores into the same slot, while the
 // softmax has step i + 1 before it, so its latency is hidden.  A product's end
@@ -182,6 +182,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// Two bf16 roundings in a word, and what a pair of values has beyond the bf16 values
+// of a word (exact for its own roundings).
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void less_bf16_pair(float x, float y, uint32_t w, float& rx, float& ry) {
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2;"
+      " fma.rn.f32.bf16 %0, l, %5, %3; fma.rn.f32.bf16 %1, h, %5, %4; }"
+      : "=f"(rx), "=f"(ry)
+      : "r"(w), "f"(x), "f"(y), "h"((uint16_t)0xbf80));  // -1
 }
 
 // One arrival for the whole warp, after all its lanes' work before it.
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
             const uint64_t z = dz + zst * (Gm::kZBytes >> 4) + (u & 1) * (64 * 128 >> 4);
 #pragma unroll
             for (int k = 0; k < (BF ? 8 : 4); ++k)
-              tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + (k & 3) * 128, id_pv, u > 0 || k > 0);
+              tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + (BF ? (k & 1) + 2 * (k >> 2) : k) * 128, id_pv, u > 0 || k > 0);
             if (u + 2 >= n2) tc_commit_to(&sfull[2 * t + (u & 1)]);
             if (u & 1) tc_commit_to(&zempty[zst]);
           }
@@ -653,12 +666,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
         tc_fence_after_sync();
         const int t0 = tc_tile(it, i0 + (u >> 1)) * 128 + 64 * (u & 1);
         const bool all_seen = t0 + 63 <= pos_a && (t0 >= lo_b || t0 + 63 < a.sink);
-        uint32_t p[BF ? 64 : 32];  // the weights, two a word; bf16: their remainders behind
-        uint64_t sum;
-        // The weights are taken against the reference at hand, with the maximum on
-        // the side; where a row has outgrown it, the warp moves it and reads S again.
+        // Where a row's maximum has outgrown its reference, the warp moves that, rescales
+        // O, and reads S again.
+        uint64_t sum = 0;
 #pragma unroll 1
-        for (int pass = 0; ok; ++pass) {
+        while (ok) {
           uint32_t sa[32], sb[32];
           tc_ld32(tu, sa);
           tc_ld32(tu + 32, sb);
@@ -674,59 +686,71 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
               if (x + 32 > me || (x + 32 < mf && x + 32 >= mg)) sb[x] = 0xff800000u;
             }
           }
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            mx4[x & 3] = max3(mx4[x & 3], __uint_as_float(sa[x]), __uint_as_float(sb[x]));
+          const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * sl;
+          const bool grow = mx > m + tc_slack<FMT>();
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(m - mx) : 1.f;
+            if (grow) m = mx;
+            if (u > 0) {
+              l *= f;
+              // the next S comes behind P Z of the step before this one
+              ok = mbar_poll(&sfull[2 * t + ((u + 1) & 1)], ((u + 1) >> 1) & 1, a.status, abrt);
+              if (!ok) break;
+              tc_fence_after_sync();
+#pragma unroll 1
+              for (int x = 0; x < RV; x += 32) {
+                uint32_t o[32];
+                tc_ld32(to + x, o);
+                tc_wait_ld(o);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tc_st32(to + x, o);
+              }
+            }
+            continue;  // (no row grows again)
+          }
           const uint32_t nb = __float_as_uint(m == -INFINITY ? 0.f : -m);
           const uint64_t nbase = pack2(nb, nb);
-          float mx = -INFINITY;
-          sum = 0;
+          // two weights a word; bf16: the remainders of 32 tokens behind their weights
           auto weights = [&](const uint32_t (&s)[32], uint32_t* out) {
 #pragma unroll
             for (int y = 0; y < 32; y += 2) {
               float p0, p1;
               unpack2(fma2(pack2(s[y], s[y + 1]), sl2, nbase), p0, p1);
-              mx = max3(mx, __uint_as_float(s[y]), __uint_as_float(s[y + 1]));
               p0 = ex2(p0);
               p1 = ex2(p1);
               sum = add2(sum, pack2(__float_as_uint(p0), __float_as_uint(p1)));
               if constexpr (BF) {
-                // the upper halves, and what they leave rounded to bf16
-                const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-                out[y / 2] = __byte_perm(b0, b1, 0x7632);
-                const __nv_bfloat162 v =
-                    __floats2bfloat162_rn(p0 - __uint_as_float(b0 & 0xffff0000u),
-                                          p1 - __uint_as_float(b1 & 0xffff0000u));
-                out[32 + y / 2] = *reinterpret_cast<const uint32_t*>(&v);
+                // the roundings, and roundings of what they leave
+                out[y / 2] = bf16_pair(p0, p1);
+                float r0, r1;
+                less_bf16_pair(p0, p1, out[y / 2], r0, r1);
+                out[16 + y / 2] = bf16_pair(r0, r1);
               } else {
                 const __half2 v = __floats2half2_rn(p0, p1);
                 out[y / 2] = *reinterpret_cast<const uint32_t*>(&v);
               }
             }
           };
-          weights(sa, p);
-          weights(sb, p + 16);
-          mx *= sl;
-          const bool grow = mx > m + tc_slack<FMT>();
-          if (pass > 0 || !__any_sync(0xffffffffu, grow)) break;
-          const float f = grow ? ex2(m - mx) : 1.f;
-          if (grow) m = mx;
-          if (u > 0) {
-            l *= f;
-            // the next S comes behind P Z of the step before this one
-            ok = mbar_poll(&sfull[2 * t + ((u + 1) & 1)], ((u + 1) >> 1) & 1, a.status, abrt);
-            if (!ok) break;
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int x = 0; x < RV; x += 32) {
-              tc_ld32(to + x, p);
-              tc_wait_ld(p);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) p[y] = __float_as_uint(__uint_as_float(p[y]) * f);
-              tc_st32(to + x, p);
-            }
+          if constexpr (BF) {
+            uint32_t p[32];
+            weights(sa, p);
+            tc_st32(tu, p);  // over S
+            weights(sb, p);
+            tc_st32(tu + 32, p);
+          } else {
+            uint32_t p[32];
+            weights(sa, p);
+            weights(sb, p + 16);
+            tc_st32(tu, p);
           }
+          break;
         }
         if (!ok) break;
-        tc_st32(tu, p);  // over S
-        if constexpr (BF) tc_st32(tu + 32, p + 32);
         float sum0, sum1;
         unpack2(sum, sum0, sum1);
         l += sum0 + sum1;
