@@ -10,10 +10,11 @@
 // where a token has few.  One row at a time a thread, at 48 resident warps:
 // more rows in flight cost registers, and so warps.
 //
-// Measured (8 x 4096 tokens, 8 KV heads, 128 + 96 + 64 columns, 193 MB each
-// way): write and read 81 us together, 4.8 TB/s; with two rows a thread 86 us, with
-// four 94, at 32 resident warps 92; blocks of four rows on CTAs of 256
-// threads, of which a token of 144 blocks left 112 idle, 106.
+// Measured (8 x 4096 tokens, 8 KV heads, 128 + 96 + 64 columns, 193 MB each way):
+// write 37 us, read 41, together 81, 4.8 TB/s where a copy reaches 6.5: the warps wait
+// for their loads, so it is bytes in flight that lack.  With two rows a thread 86 us,
+// with four 94, at 32 resident warps 92; blocks of four rows on CTAs of 256 threads,
+// of which a token of 144 blocks left 112 idle, 106.
 #include "cache4.cuh"
 #include "common.cuh"
 #include "internal.h"

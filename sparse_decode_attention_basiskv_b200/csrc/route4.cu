@@ -4,9 +4,8 @@
 //                 z_t . (P_K q_h) + e_t . (U_K^T q_h)
 //
 // with the folded queries in fp32 (fold_query_kernel).  One pass over the z
-// and e pages: (r_v + r_k) * 9 / 16 bytes a token and KV head, so HBM bounds
-// it, closely followed by the instructions that widen the codes (a conversion
-// and a multiplication for two columns).
+// and e pages: (r_v + r_k) * 9 / 16 bytes a token and KV head, and a conversion
+// and a multiplication for two columns to widen the codes.
 //
 // The units (32 tokens: one page of 32 or two of 16) of all (sequence, KV
 // head) items form one line, cut into equal contiguous runs, one a warp (a
@@ -21,9 +20,12 @@
 // largest magnitude into [2^14, 2^15), divided out of the scores again).
 //
 // Measured: 16 x 32K tokens, 8 KV heads, r_v 64, r_k 32 (228 MB): 64 us with the
-// folding of the queries, 3.6 TB/s; the widening's instructions bound it (68% of
-// the issue slots).  Rings with one unit requested at a time took 70 us, a fourth of the warps as
-// loaders for the others 101 us, two CTAs an SM instead of three 65 us.
+// folding of the queries, 3.6 TB/s (69 with the selection behind it).  Neither HBM
+// nor the issue slots (68%) are full: with the conversions taken out it takes 62
+// us, with the multiplications 57, with both 55, so what is left is the latency of
+// a unit's chain of loads and products.  Rings with one unit requested at a time
+// took 70 us, a fourth of the warps as loaders for the others 101 us, two CTAs an SM
+// instead of three 65 us.
 #include "cache4.cuh"
 #include "common.cuh"
 #include "internal.h"

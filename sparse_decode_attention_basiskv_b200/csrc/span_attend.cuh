@@ -8,9 +8,9 @@
 // Rows: query token j and head h of KV head g make row j * G + h; up to 32 rows
 // (one to four N tiles of mma.m16n8k16) share every Key and latent that is
 // read.
-// Bound by HBM: 2 (d + r_v) multiply-adds a row and (d + r_v) cached columns
-// a token; over 4-bit caches closely followed by the instructions that widen
-// the codes (a conversion and a multiplication for two columns).
+// Bound by HBM: 2 (d + r_v) multiply-adds a row and (d + r_v) cached columns a token;
+// over 4-bit caches as much by the chain of a unit, in which the codes are widened (a
+// conversion and a multiplication for two columns).
 //
 // Split: the unit of work is 16 tokens (4-bit caches: 32).  All units of all
 // (sequence, KV head) items form one line in (b, g, unit) order, cut into
@@ -40,13 +40,14 @@
 // one vote.
 //
 // Precision: scores and sums in fp32.  The weights of PV are rounded to f16
-// (2^-12 of each weight, an eighth of the output's own rounding) where the
+// (2^-11 of each weight, an eighth of the output's own rounding) where the
 // operands are f16, and held as bf16 roundings plus bf16 remainders (16
 // significant bits, a second product) where they are bf16.
 //
 // Measured (16 x 32K tokens, 8 KV heads, d 128, r_v 64, G 4): bf16, window 4096
-// (202 MB) 42 us, 4.8 TB/s; 4 bits, all tokens (453 MB) 114 us, 4.0 TB/s, bound
-// by issue slots (62% used) and the conversions' pipe; 128 selected
+// (202 MB) 42 us, 4.8 TB/s; E4M3, the same 30 us, all tokens (806 MB) 135, 6.0 TB/s; 4
+// bits, all tokens (453 MB) 110 us, 4.1 TB/s, with neither HBM nor the issue slots
+// (62%) full: without the conversions 107, without the scales' products 94; 128 selected
 // pages of 4 bits (28 MB) 19 us, a start of 8 us and one turn of the ring;
 // E4M3, 7 ragged sequences, window 8192, 20 rows (89 MB) 41 us against 69 on
 // the prompt kernel.  Joining the partials of an item with one CTA took 23 us

@@ -27,31 +27,32 @@
 // ahead of what they hand over.
 //
 // Precision: scores, maxima and sums in fp32.  Over E4M3 and 4-bit caches the weights
-// are rounded to f16 for P Z (2^-12 of a weight).  Over bf16 ones a weight is its bf16
+// are rounded to f16 for P Z (2^-11 of a weight).  Over bf16 ones a weight is its bf16
 // rounding and a rounding of the rest (16 bits, a second product), so that a prompt is
 // as accurate as a token.  With weights of 8 bits the chunk below takes 273 us instead
 // of 305, and its error against 64 bits is 2.2e-3 instead of 1.7e-3, of which 1.7e-3 is
 // the output's rounding; with a row's sum taken over such weights (which makes rows
 // of one large weight exact) it takes 296.
 //
-// Tensor memory: per row tile two slots of 64 columns for S, P over its S (bf16: 32
-// tokens' weights, their remainders, the other 32 tokens'), r_v for O, and Q in what is left (all of it for r_v up to 64, d
-// 128; the other k-steps read Q from shared memory).  Q K^T of step i + 2
-// follows P Z of step i on the tensor cores into the same slot, while the
-// softmax has step i + 1 before it, so its latency is hidden.  A product's end
-// needs no barrier of its own: S of step i + 2 is behind P Z of step i, so its
-// barrier tells both (a wait costs some 270 clocks even when the phase is
-// over; one a step less took the chunk below from 305 to 282 us).
+// Tensor memory: per row tile two slots of 64 columns for S, P over its S (bf16:
+// 32 tokens' weights, their remainders, the other 32 tokens'), r_v for O, and Q in
+// what is left (all of it for r_v up to 64, d 128, half at 96, none at 128; the other
+// k-steps read Q from shared memory).  Q K^T of step i + 2 follows P Z of step i on
+// the tensor cores into the same slot, while the softmax has step i + 1 before it,
+// so its latency is hidden.  A product's end needs no barrier of its own: S of step
+// i + 2 is behind P Z of step i, so its barrier tells both (a wait costs some 270
+// clocks even when the phase is over; one a step less was worth 8%).
 //
-// Measured (4096-token chunk, Llama-8B layer, window 4096, bf16): 282 us, 731
-// TFLOP/s.  Three ragged sequences of 1023 tokens, Qwen3-32B layer, window
-// 2000, 4 bits: 274 us, 643 TFLOP/s.  Bound by the softmax's chain of a step:
-// load, weights, store, two barriers, 1750 clocks where its exponentials take
-// 1020; without the exponentials the chunk takes 255 us, with a quarter of the
-// products 273, without the copies 262.  An item's start (queries to tensor memory, the
-// first tile, and the first step twice, for its reference) costs some 10,000 clocks.  One
-// slot of 128 columns a row tile, the softmax waiting for each product, was 7%
-// slower.
+// Measured (4096-token chunk, Llama-8B layer, window 4096, inputs past L2): bf16 326
+// us, 633 TFLOP/s; the same inputs again and again 300, r_v 128 405, E4M3 285, r_v 128
+// 416, 4 bits 286, r_v 128 321.  Three ragged sequences of 1023 tokens, Qwen3-32B
+// layer, window 2000, 4 bits: 275 us, 641 TFLOP/s.  Bound by the softmax's chain of a
+// step: load, maximum, weights, store, two barriers, some 1950 clocks (bf16) where its
+// exponentials take 1020: with weights of 8 bits (1750 clocks, 282 us) the chunk took
+// 255 without the exponentials, 273 with a quarter of the products and 262 without
+// the copies.  An item's start (queries to tensor memory, the first tile) costs some
+// 10,000 clocks.  One slot of 128 columns a row tile, the softmax waiting for each
+// product, was 7% slower.
 //
 // Tokens whose block-table entry is out of range have no part in the softmax: the
 // issuing warp, which looks the run's entries up at the start, sets their scores to
@@ -315,8 +316,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
       };
       bool gap = false;  // (looked up while the first tile is on its way)
       const int lp = 7 - a.logS;  // log2 of a tile's pages
-      for (int x = lane; x < n << lp; x += 32)
-        gap |= missing((tc_tile(it, i0 + (x >> lp)) * 128) + ((x & ((1 << lp) - 1)) << a.logS), a.S);
+      for (int x = lane; x < n << lp; x += 32) {
+        const int page = x & ((1 << lp) - 1);
+        gap |= missing(tc_tile(it, i0 + (x >> lp)) * 128 + (page << a.logS), a.S);
+      }
       gap = __any_sync(0xffffffffu, gap);
       int scored_ph = 0;
       auto issue = [&](auto gaps) {
@@ -333,7 +336,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
               if (k < Gm::kQSteps)
                 tc_mma_ts(tm_s + 64 * (u & 1), tm_q + 8 * k, kk, id_qk, k > 0);
               else
-                tc_mma_ss(tm_s + 64 * (u & 1), dq + (k >> 2) * 1024 + (k & 3) * 2, kk, id_qk, k > 0);
+                tc_mma_ss(tm_s + 64 * (u & 1), dq + (k >> 2) * 1024 + (k & 3) * 2, kk, id_qk,
+                          k > 0);
             }
           }
           if constexpr (GAPS) {
@@ -379,8 +383,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) span_tc_kernel(SpanArgs a, TcPl
           if (lead) {
             const uint64_t z = dz + zst * (Gm::kZBytes >> 4) + (u & 1) * (64 * 128 >> 4);
 #pragma unroll
-            for (int k = 0; k < (BF ? 8 : 4); ++k)
-              tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + (BF ? (k & 1) + 2 * (k >> 2) : k) * 128, id_pv, u > 0 || k > 0);
+            for (int k = 0; k < (BF ? 8 : 4); ++k) {
+              const int zk = BF ? (k & 1) + 2 * (k >> 2) : k;  // (remainders: k 2, 3, 6, 7)
+              tc_mma_ts(tm_o, tm_s + 64 * (u & 1) + 8 * k, z + zk * 128, id_pv, u > 0 || k > 0);
+            }
             if (u + 2 >= n2) tc_commit_to(&sfull[2 * t + (u & 1)]);
             if (u & 1) tc_commit_to(&zempty[zst]);
           }

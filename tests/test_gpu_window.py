@@ -365,3 +365,14 @@ def test_drafts_whose_bound_passes_the_contexts(fmt, bound, G, d, rv, page, n):
     p.run()
     assert bkv.read_device_status() == 0
     p.check(kind="bf16_token" if fmt == "bf16" else fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [1, 6, 24, 200])
+def test_the_same_call_gives_the_same_bits(fmt, n):
+    p = _go(fmt, 4, 4, 4, 128, 64, 16, [1500, 90, 1333, 700], n, 600, 4)
+    first = p.out.clone()
+    for fill in (0x00, 0x3C, 0x7F):
+        p.ws.fill_(fill)
+        p.out.fill_(3.0)
+        assert torch.equal(p.run(), first)
