@@ -30,9 +30,8 @@
 // are rounded to f16 for P Z (2^-11 of a weight).  Over bf16 ones a weight is its bf16
 // rounding and a rounding of the rest (16 bits, a second product), so that a prompt is
 // as accurate as a token.  With weights of 8 bits the chunk below takes 270 us instead
-// of 300 (the same inputs again and again), and its error against 64 bits is 2.2e-3 instead of 1.7e-3, of which 1.7e-3 is
-// the output's rounding; with a row's sum taken over such weights (which makes rows
-// of one large weight exact) it takes 296.
+// of 300 (the same inputs again and again), and its error against 64 bits is 2.2e-3
+// instead of 1.7e-3, the output's own rounding.
 //
 // Tensor memory: per row tile two slots of 64 columns for S, P over its S (bf16:
 // 32 tokens' weights, their remainders, the other 32 tokens'), r_v for O, and Q in
